@@ -258,8 +258,7 @@ def prepare(c, seed):
         from bit_mixed_precision_channel_b200 import binding as kb
 
         cfg = kb.Config(num_q_heads=H * gq, num_kv_heads=H, page_tokens=P, num_boost=k, dtype=kb.BF16 if dt == torch.bfloat16 else kb.F16)
-        size = {"select": lambda: kb.select_workspace_bytes(cfg, B, N), "sparse": lambda: kb.decode_workspace_bytes(cfg, B, N),
-                "tree": lambda: kb.tree_workspace_bytes(cfg, B, T), "append": lambda: 0}[c["op"]]()
+        size = kb.decode_workspace_bytes(cfg, B, N) if c["op"] == "sparse" else kb.tree_workspace_bytes(cfg, B, T) if c["op"] == "tree" else 0
         s["cfg"], s["workspace"] = cfg, torch.zeros(max(size, 256), dtype=torch.uint8, device=dev)
         s["err"] = torch.zeros(1, dtype=torch.int32, device=dev)
     return s
@@ -422,7 +421,7 @@ def run(s):
         from bit_mixed_precision_channel_b200 import binding as kb
 
         if c["op"] == "select":
-            kb.select_pages(s["cfg"], s["pool"], s["q"], s["page_table"], s["num_pages"], s["sel"], s["n_sel"], s["workspace"],
+            kb.select_pages(s["cfg"], s["pool"], s["q"], s["page_table"], s["num_pages"], s["sel"], s["n_sel"],
                             n_first=c["first"], n_recent=c["recent"], err=s["err"])
         elif c["op"] == "sparse":
             kb.decode_attention_sparse(s["cfg"], s["pool"], s["q"], s["page_table"], s["num_pages"], s["sel"], s["n_sel"], s["res_k"],
