@@ -21,6 +21,7 @@ __all__ = [
     "quantize_values", "quantize_pages", "append_token", "flush_residual",
     "decode_workspace_bytes", "decode_attention", "decode_attention_static", "STATIC_SCRATCH_BYTES",
     "quantize_pages_ex", "dense_page_bytes", "decode_attention_dense",
+    "select_pages", "decode_attention_sparse", "tree_workspace_bytes", "tree_attention", "append_path", "MAX_DRAFT",
     "prefill_workspace_bytes", "prefill_attention", "retain_tokens", "gather_tokens",
     "F16", "BF16", "torch_dtype",
     "DEV_ERR_PAGE_RANGE", "DEV_ERR_RESIDUAL", "DEV_ERR_TABLE_FULL", "DEV_ERR_TIMEOUT",
@@ -36,6 +37,7 @@ DEV_ERR_TIMEOUT = 8
 DEV_ERR_LENGTH = 16
 DEV_ERR_RANGE = 32
 STATIC_SCRATCH_BYTES = 16 << 20  # KVQ_STATIC_SCRATCH_BYTES
+MAX_DRAFT = 128  # KVQ_MAX_DRAFT
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -159,6 +161,19 @@ def load():
         L.kvq_decode_attention_dense.restype = ctypes.c_int
         L.kvq_decode_attention_dense.argtypes = [cfgp, vp, i64, vp, i32, vp, i32, vp, ctypes.c_float, vp, vp, sz,
                                                  vp, vp]
+        f32 = ctypes.c_float
+        L.kvq_select_pages.restype = ctypes.c_int
+        L.kvq_select_pages.argtypes = [cfgp, vp, i64, vp, i32, vp, i32, vp, i32, i32, i32, vp, vp, vp, vp]
+        L.kvq_decode_attention_sparse.restype = ctypes.c_int
+        L.kvq_decode_attention_sparse.argtypes = [cfgp, vp, i64, vp, i32, vp, i32, vp, vp, i32, vp, vp, vp, vp, f32,
+                                                  vp, vp, sz, vp, vp]
+        L.kvq_tree_workspace_bytes.restype = sz
+        L.kvq_tree_workspace_bytes.argtypes = [cfgp, i32, i32]
+        L.kvq_tree_attention.restype = ctypes.c_int
+        L.kvq_tree_attention.argtypes = [cfgp, vp, i64, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, f32,
+                                         vp, vp, sz, vp, vp]
+        L.kvq_append_path.restype = ctypes.c_int
+        L.kvq_append_path.argtypes = [cfgp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
         L.kvq_prefill_workspace_bytes.restype = sz
         L.kvq_prefill_workspace_bytes.argtypes = [cfgp, i32]
         L.kvq_prefill_attention.restype = ctypes.c_int
@@ -263,6 +278,10 @@ def page_layout(cfg: Config) -> dict:
 
 def page_bytes(cfg: Config) -> int:
     return int(load().kvq_page_bytes(ctypes.byref(cfg.c())))
+
+
+def _pool_pages(cfg: Config, pool: torch.Tensor) -> int:
+    return pool.numel() // (cfg.num_kv_heads * page_bytes(cfg))
 
 
 def _boost_options(cfg: Config, query_weight, boost_per_head):
@@ -446,6 +465,107 @@ def decode_attention_static(cfg: Config, pool, q, page_table, num_pages, res_k, 
         ctypes.byref(cfg.c()), pool.data_ptr(), pool_pages, q.data_ptr(), batch, page_table.data_ptr(),
         max_pages, num_pages.data_ptr(), res_k.data_ptr(), res_v.data_ptr(), res_len.data_ptr(),
         float(sm_scale), out.data_ptr(), _ptr(err), _stream(stream)))
+
+
+def select_pages(cfg: Config, pool, q, page_table, num_pages, sel, n_sel, n_first: int = 0, n_recent: int = 0,
+                 err=None, stream=None):
+    """Chooses the pages a decode step reads: sel int32 [B][Hkv][n_select] receives the slots
+    of the page table with the largest logit bounds (the first n_first and the last n_recent
+    pages always), ascending, then -1; n_sel int32 [B] their number."""
+    _need("page_table", page_table, torch.int32, dim=2)
+    batch, max_pages = page_table.shape
+    _need("sel", sel, torch.int32, dim=3)
+    if sel.shape[0] != batch or sel.shape[1] != cfg.num_kv_heads:
+        raise ValueError(f"sel: shape {tuple(sel.shape)}, the call writes [{batch}][{cfg.num_kv_heads}][n_select]")
+    _need("pool", pool, torch.uint8)
+    _need("q", q, torch_dtype(cfg.dtype), batch * cfg.num_q_heads * cfg.head_dim)
+    _need("num_pages", num_pages, torch.int32, batch)
+    _need("n_sel", n_sel, torch.int32, batch)
+    _need("err", err, torch.int32, 1)
+    _cuda(pool, q, page_table, num_pages, sel, n_sel, err, stream=stream)
+    _check("kvq_select_pages", load().kvq_select_pages(
+        ctypes.byref(cfg.c()), pool.data_ptr(), _pool_pages(cfg, pool), q.data_ptr(), batch, page_table.data_ptr(),
+        max_pages, num_pages.data_ptr(), n_first, n_recent, sel.shape[2], sel.data_ptr(), n_sel.data_ptr(), _ptr(err),
+        _stream(stream)))
+
+
+def decode_attention_sparse(cfg: Config, pool, q, page_table, num_pages, sel, n_sel, res_k, res_v, res_len, out,
+                            workspace, sm_scale: float | None = None, err=None, stream=None):
+    """decode_attention over the pages in slots sel[b][kv head][:n_sel[b]] of the page table
+    (sel int32 [B][Hkv][max_sel]) and the residual window."""
+    _need_decode(cfg, pool, q, page_table, num_pages, res_k, res_v, res_len, out, err)
+    batch, max_pages = page_table.shape
+    _need("sel", sel, torch.int32, dim=3)
+    if sel.shape[0] != batch or sel.shape[1] != cfg.num_kv_heads:
+        raise ValueError(f"sel: shape {tuple(sel.shape)}, the call reads [{batch}][{cfg.num_kv_heads}][max_sel]")
+    _need("n_sel", n_sel, torch.int32, batch)
+    _need("workspace", workspace, torch.uint8)
+    _cuda(pool, q, page_table, num_pages, sel, n_sel, res_k, res_v, res_len, out, workspace, err, stream=stream)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(cfg.head_dim)
+    _check("kvq_decode_attention_sparse", load().kvq_decode_attention_sparse(
+        ctypes.byref(cfg.c()), pool.data_ptr(), _pool_pages(cfg, pool), q.data_ptr(), batch, page_table.data_ptr(),
+        max_pages, num_pages.data_ptr(), sel.data_ptr(), sel.shape[2], n_sel.data_ptr(), res_k.data_ptr(),
+        res_v.data_ptr(), res_len.data_ptr(), float(sm_scale), out.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _ptr(err), _stream(stream)))
+
+
+def tree_workspace_bytes(cfg: Config, batch: int, n_draft: int) -> int:
+    return int(load().kvq_tree_workspace_bytes(ctypes.byref(cfg.c()), batch, n_draft))
+
+
+def tree_attention(cfg: Config, pool, q, page_table, num_pages, res_k, res_v, res_len, k_draft, v_draft, mask,
+                   draft_len, out, workspace, sm_scale: float | None = None, err=None, stream=None):
+    """Attention of drafted tokens over pages, residual window and the drafted tokens their
+    mask names: q [B][T][Hq][D], k_draft and v_draft [B][T][Hkv][D] of the cache dtype, mask
+    int32 [B][T][ceil(T/32)] (bit j % 32 of word j // 32), draft_len int32 [B], out fp32
+    [B][T][Hq][D] (rows at or past draft_len[b] are left as they were)."""
+    dt, H, P, D = torch_dtype(cfg.dtype), cfg.num_kv_heads, cfg.page_tokens, cfg.head_dim
+    _need("page_table", page_table, torch.int32, dim=2)
+    batch, max_pages = page_table.shape
+    _need("q", q, dt, dim=4)
+    T = q.shape[1]
+    _need("q", q, dt, batch * T * cfg.num_q_heads * D)
+    _need("k_draft", k_draft, dt, batch * T * H * D)
+    _need("v_draft", v_draft, dt, batch * T * H * D)
+    _need("mask", mask, torch.int32, batch * T * ((T + 31) // 32))
+    _need("draft_len", draft_len, torch.int32, batch)
+    _need("out", out, torch.float32, batch * T * cfg.num_q_heads * D)
+    _need("pool", pool, torch.uint8)
+    _need("num_pages", num_pages, torch.int32, batch)
+    _need("res_len", res_len, torch.int32, batch)
+    _need("res_k", res_k, dt, batch * H * P * D)
+    _need("res_v", res_v, dt, batch * H * P * D)
+    _need("workspace", workspace, torch.uint8)
+    _need("err", err, torch.int32, 1)
+    _cuda(pool, q, page_table, num_pages, res_k, res_v, res_len, k_draft, v_draft, mask, draft_len, out, workspace,
+          err, stream=stream)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    _check("kvq_tree_attention", load().kvq_tree_attention(
+        ctypes.byref(cfg.c()), pool.data_ptr(), _pool_pages(cfg, pool), q.data_ptr(), T, batch, page_table.data_ptr(),
+        max_pages, num_pages.data_ptr(), res_k.data_ptr(), res_v.data_ptr(), res_len.data_ptr(), k_draft.data_ptr(),
+        v_draft.data_ptr(), mask.data_ptr(), draft_len.data_ptr(), float(sm_scale), out.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _ptr(err), _stream(stream)))
+
+
+def append_path(cfg: Config, k_draft, v_draft, path, n_path, taken, res_k, res_v, res_len, err=None, stream=None):
+    """Tokens path[b][taken[b]:n_path[b]] of k_draft and v_draft [B][T][Hkv][D] behind the
+    residual window, as many as fit; res_len and taken (int32 [B]) advance by that number."""
+    dt, H, P, D = torch_dtype(cfg.dtype), cfg.num_kv_heads, cfg.page_tokens, cfg.head_dim
+    _need("path", path, torch.int32, dim=2)
+    batch, T = path.shape
+    _need("k_draft", k_draft, dt, batch * T * H * D)
+    _need("v_draft", v_draft, dt, batch * T * H * D)
+    for name, t in (("n_path", n_path), ("taken", taken), ("res_len", res_len)):
+        _need(name, t, torch.int32, batch)
+    _need("res_k", res_k, dt, batch * H * P * D)
+    _need("res_v", res_v, dt, batch * H * P * D)
+    _need("err", err, torch.int32, 1)
+    _cuda(k_draft, v_draft, path, n_path, taken, res_k, res_v, res_len, err, stream=stream)
+    _check("kvq_append_path", load().kvq_append_path(
+        ctypes.byref(cfg.c()), batch, T, k_draft.data_ptr(), v_draft.data_ptr(), path.data_ptr(), n_path.data_ptr(),
+        taken.data_ptr(), res_k.data_ptr(), res_v.data_ptr(), res_len.data_ptr(), _ptr(err), _stream(stream)))
 
 
 def dense_page_bytes(cfg: Config) -> int:

@@ -67,6 +67,34 @@ kvq_status decode_check_args(const kvq_config* cfg, const void* pool, int64_t po
   return KVQ_OK;
 }
 
+// The decode parameters that do not depend on how the pages are listed.
+static DecodeParams decode_params(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q, int batch,
+                                  const void* res_k, const void* res_v, const int32_t* res_len, float sm_scale,
+                                  float* out, void* workspace, const Plan& pl, int32_t* err) {
+  DecodeParams p{};
+  p.pool = static_cast<const uint8_t*>(pool);
+  p.pool_pages = pool_pages;
+  p.Hkv = cfg->num_kv_heads;
+  p.P = cfg->page_tokens;
+  p.k = cfg->num_boost;
+  p.KB = cfg->num_boost / 16;
+  p.L = make_layout(cfg->page_tokens, cfg->head_dim, cfg->num_boost, cfg->key_group);
+  p.q = static_cast<const uint16_t*>(q);
+  p.batch = batch;
+  p.Hq = cfg->num_q_heads;
+  p.res_k = static_cast<const uint16_t*>(res_k);
+  p.res_v = static_cast<const uint16_t*>(res_v);
+  p.res_len = res_len;
+  p.c_log2 = sm_scale * 1.4426950408889634f;
+  p.out = out;
+  p.part = static_cast<float*>(workspace);
+  p.cnt = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + pl.part_bytes);
+  p.n_ctas = pl.ctas;
+  p.n_sms = sm_count();
+  p.err = err;
+  return p;
+}
+
 }  // namespace kvq
 
 using namespace kvq;
@@ -331,31 +359,137 @@ kvq_status kvq_decode_attention(const kvq_config* cfg, const void* pool, int64_t
   const Plan pl = decode_plan(cfg, batch);
   if (workspace_bytes < pl.part_bytes + pl.cnt_bytes) return KVQ_ERR_CAPACITY;
   const int gqa = cfg->num_q_heads / cfg->num_kv_heads;
-  DecodeParams p{};
+  DecodeParams p = decode_params(cfg, pool, pool_pages, q, batch, res_k, res_v, res_len, sm_scale, out, workspace, pl,
+                                 err);
+  p.page_table = page_table;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  return cuda_status(launch_decode(p, gqa, cfg->dtype, stream));
+}
+
+kvq_status kvq_decode_attention_sparse(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
+                                       int32_t batch, const int32_t* page_table, int32_t max_pages,
+                                       const int32_t* num_pages, const int32_t* sel, int32_t max_sel,
+                                       const int32_t* n_sel, const void* res_k, const void* res_v,
+                                       const int32_t* res_len, float sm_scale, float* out, void* workspace,
+                                       size_t workspace_bytes, int32_t* err, cudaStream_t stream) {
+  const kvq_status s = decode_check_args(cfg, pool, pool_pages, q, batch, sel, max_sel, n_sel, res_k, res_v, res_len,
+                                         out);
+  if (s != KVQ_OK) return s;
+  if (max_pages < 0) return KVQ_ERR_INVALID_ARG;
+  if (batch == 0) return KVQ_OK;
+  if (!num_pages || (max_sel > 0 && max_pages > 0 && !page_table)) return KVQ_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
+  const Plan pl = decode_plan(cfg, batch);
+  if (workspace_bytes < pl.part_bytes + pl.cnt_bytes) return KVQ_ERR_CAPACITY;
+  DecodeParams p = decode_params(cfg, pool, pool_pages, q, batch, res_k, res_v, res_len, sm_scale, out, workspace, pl,
+                                 err);
+  p.page_table = page_table;
+  p.max_pages = max_sel;
+  p.num_pages = n_sel;
+  p.sel = sel;
+  p.table_len = num_pages;
+  p.table_pages = max_pages;
+  return cuda_status(launch_decode(p, cfg->num_q_heads / cfg->num_kv_heads, cfg->dtype, stream));
+}
+
+kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q, int32_t batch,
+                            const int32_t* page_table, int32_t max_pages, const int32_t* num_pages, int32_t n_first,
+                            int32_t n_recent, int32_t n_select, int32_t* sel, int32_t* n_sel, int32_t* err,
+                            cudaStream_t stream) {
+  const kvq_status s = kvq_check_config(cfg);
+  if (s != KVQ_OK) return s;
+  if (batch < 0 || max_pages < 0 || n_first < 0 || n_recent < 0 || n_select < 1) return KVQ_ERR_INVALID_ARG;
+  if ((long long)n_first + n_recent > n_select) return KVQ_ERR_INVALID_ARG;
+  if (batch == 0) return KVQ_OK;
+  if (!pool || pool_pages <= 0 || !q || !num_pages || !sel || !n_sel) return KVQ_ERR_INVALID_ARG;
+  if (max_pages > 0 && !page_table) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(pool) || !aligned16(q)) return KVQ_ERR_INVALID_ARG;
+  if (max_pages > kSelectMaxPages) return KVQ_ERR_UNSUPPORTED;
+  if ((long long)batch * cfg->num_kv_heads > (1ll << 27)) return KVQ_ERR_INVALID_ARG;  // 8 CTAs each in one grid
+  SelectParams p{};
   p.pool = static_cast<const uint8_t*>(pool);
   p.pool_pages = pool_pages;
   p.Hkv = cfg->num_kv_heads;
-  p.P = cfg->page_tokens;
+  p.gqa = cfg->num_q_heads / cfg->num_kv_heads;
   p.k = cfg->num_boost;
-  p.KB = cfg->num_boost / 16;
+  p.batch = batch;
+  p.max_pages = max_pages;
   p.L = make_layout(cfg->page_tokens, cfg->head_dim, cfg->num_boost, cfg->key_group);
   p.q = static_cast<const uint16_t*>(q);
-  p.batch = batch;
-  p.Hq = cfg->num_q_heads;
   p.page_table = page_table;
+  p.num_pages = num_pages;
+  p.n_first = n_first;
+  p.n_recent = n_recent;
+  p.n_select = n_select;
+  p.sel = sel;
+  p.n_sel = n_sel;
+  p.err = err;
+  return cuda_status(launch_select_pages(p, cfg->page_tokens, cfg->dtype, stream));
+}
+
+size_t kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n_draft) {
+  if (kvq_check_config(cfg) != KVQ_OK || batch < 0 || n_draft < 1 || n_draft > KVQ_MAX_DRAFT) return 0;
+  return 256;
+}
+
+kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
+                              int32_t n_draft, int32_t batch, const int32_t* page_table, int32_t max_pages,
+                              const int32_t* num_pages, const void* res_k, const void* res_v, const int32_t* res_len,
+                              const void* k_draft, const void* v_draft, const uint32_t* mask,
+                              const int32_t* draft_len, float sm_scale, float* out, void* workspace,
+                              size_t workspace_bytes, int32_t* err, cudaStream_t stream) {
+  const kvq_status s = decode_check_args(cfg, pool, pool_pages, q, batch, page_table, max_pages, num_pages, res_k,
+                                         res_v, res_len, out);
+  if (s != KVQ_OK) return s;
+  if (n_draft < 1) return KVQ_ERR_INVALID_ARG;
+  if (n_draft > KVQ_MAX_DRAFT) return KVQ_ERR_UNSUPPORTED;
+  if (batch == 0) return KVQ_OK;
+  if (!k_draft || !v_draft || !mask || !draft_len || !workspace) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(k_draft) || !aligned16(v_draft) || !aligned16(out) || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
+  if (batch > 65535 || cfg->num_q_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (workspace_bytes < kvq_tree_workspace_bytes(cfg, batch, n_draft)) return KVQ_ERR_CAPACITY;
+  TreeParams p{};
+  p.pool = static_cast<const uint8_t*>(pool);
+  p.pool_pages = pool_pages;
+  p.Hkv = cfg->num_kv_heads;
+  p.Hq = cfg->num_q_heads;
+  p.gqa = cfg->num_q_heads / cfg->num_kv_heads;
+  p.P = cfg->page_tokens;
+  p.k = cfg->num_boost;
+  p.batch = batch;
   p.max_pages = max_pages;
+  p.T = n_draft;
+  p.W = (n_draft + 31) / 32;
+  p.L = make_layout(cfg->page_tokens, cfg->head_dim, cfg->num_boost, cfg->key_group);
+  p.q = static_cast<const uint16_t*>(q);
+  p.page_table = page_table;
   p.num_pages = num_pages;
   p.res_k = static_cast<const uint16_t*>(res_k);
   p.res_v = static_cast<const uint16_t*>(res_v);
   p.res_len = res_len;
+  p.k_draft = static_cast<const uint16_t*>(k_draft);
+  p.v_draft = static_cast<const uint16_t*>(v_draft);
+  p.mask = mask;
+  p.draft_len = draft_len;
   p.c_log2 = sm_scale * 1.4426950408889634f;
   p.out = out;
-  p.part = static_cast<float*>(workspace);
-  p.cnt = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + pl.part_bytes);
-  p.n_ctas = pl.ctas;
-  p.n_sms = sm_count();
   p.err = err;
-  return cuda_status(launch_decode(p, gqa, cfg->dtype, stream));
+  return cuda_status(launch_tree(p, cfg->dtype, stream));
+}
+
+kvq_status kvq_append_path(const kvq_config* cfg, int32_t batch, int32_t n_draft, const void* k_draft,
+                           const void* v_draft, const int32_t* path, const int32_t* n_path, int32_t* taken,
+                           void* res_k, void* res_v, int32_t* res_len, int32_t* err, cudaStream_t stream) {
+  const kvq_status s = kvq_check_config(cfg);
+  if (s != KVQ_OK) return s;
+  if (batch < 0 || n_draft < 1) return KVQ_ERR_INVALID_ARG;
+  if (n_draft > KVQ_MAX_DRAFT) return KVQ_ERR_UNSUPPORTED;
+  if (batch == 0) return KVQ_OK;
+  if (!k_draft || !v_draft || !path || !n_path || !taken || !res_k || !res_v || !res_len) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(k_draft) || !aligned16(v_draft) || !aligned16(res_k) || !aligned16(res_v)) return KVQ_ERR_INVALID_ARG;
+  return cuda_status(launch_append_path(k_draft, v_draft, path, n_path, taken, n_draft, res_k, res_v, res_len, batch,
+                                        cfg->num_kv_heads, cfg->page_tokens, err, stream));
 }
 
 size_t kvq_prefill_workspace_bytes(const kvq_config* cfg, int32_t L) {

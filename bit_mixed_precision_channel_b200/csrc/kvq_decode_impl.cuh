@@ -810,7 +810,14 @@ __device__ __forceinline__ void build_segment(const DecodeParams& p, CtaShared<G
       const int npg = min(PPC, sp.np - k * PPC);
       w |= uint32_t(npg) | (uint32_t(k) << 16);
       for (int i = 0; i < npg; ++i) {
-        int id = __ldcg(p.page_table + size_t(sp.b) * p.max_pages + k * PPC + i);
+        int id;
+        if (p.sel) {  // the chosen slot of this kv head, then the page it holds
+          const int slot = __ldcg(p.sel + (size_t(sp.b) * p.Hkv + sp.h) * p.max_pages + k * PPC + i);
+          const int len = min(__ldcg(p.table_len + sp.b), p.table_pages);
+          id = slot >= 0 && slot < len ? __ldcg(p.page_table + size_t(sp.b) * p.table_pages + slot) : -1;
+        } else {
+          id = __ldcg(p.page_table + size_t(sp.b) * p.max_pages + k * PPC + i);
+        }
         if (id < 0 || id >= p.pool_pages) {
           flag_error(p.err, KVQ_DEV_ERR_PAGE_RANGE);
           id = 0;

@@ -25,6 +25,7 @@ constexpr int kDecodeMergeWeight = 6;
 constexpr int kHeadDim = 128;
 constexpr int kKeyGroup = 32;
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kSelectMaxPages = 8 * 25600;  // keys of a cluster's 8 CTAs, 200 KB of shared memory each
 
 // Byte offsets of one (page, kv head) record.  Section order and sizes follow the
 // page-record description in kvq.h: plane A codes, plane B codes, value codes, plane-A
@@ -344,11 +345,59 @@ struct DecodeParams {
   // dense mode: tokens per sequence; pool then holds raw pages [pool_pages][Hkv][2][P][128]
   // (K rows, V rows) of the cache dtype, and num_pages / res_len / res_k / res_v are unused
   const int32_t* seq_len;
+  // sparse mode: the slots of the page table each (sequence, kv head) attends to,
+  // [batch][Hkv][max_pages]; num_pages then counts the slots, and the table itself has
+  // table_pages entries a sequence, table_len[b] of them in use
+  const int32_t* sel;
+  const int32_t* table_len;
+  int table_pages;
+};
+
+// Choice of pages by the largest logits their key ranges allow.
+struct SelectParams {
+  const uint8_t* pool;
+  long long pool_pages;
+  int Hkv, gqa, k, batch, max_pages;
+  Layout L;
+  const uint16_t* q;
+  const int32_t* page_table;
+  const int32_t* num_pages;
+  int n_first, n_recent, n_select;
+  int32_t* sel;    // [batch][Hkv][n_select]
+  int32_t* n_sel;  // [batch]
+  int32_t* err;
+};
+
+// Attention of a tree of drafted tokens.
+struct TreeParams {
+  const uint8_t* pool;
+  long long pool_pages;
+  int Hkv, Hq, gqa, P, k, batch, max_pages;
+  int T, W;  // drafted tokens, 32-bit mask words a token
+  Layout L;
+  const uint16_t* q;  // [batch][T][Hq][128]
+  const int32_t* page_table;
+  const int32_t* num_pages;
+  const uint16_t* res_k;
+  const uint16_t* res_v;
+  const int32_t* res_len;
+  const uint16_t* k_draft;  // [batch][T][Hkv][128]
+  const uint16_t* v_draft;
+  const uint32_t* mask;  // [batch][T][W]
+  const int32_t* draft_len;
+  float c_log2;
+  float* out;  // [batch][T][Hq][128]
+  int32_t* err;
 };
 
 cudaError_t launch_quantize(const QuantParams& p, int n_items, int dtype, cudaStream_t stream);
 cudaError_t launch_append(const void* k_new, const void* v_new, void* res_k, void* res_v, int32_t* res_len,
                           int batch, int Hkv, int P, int32_t* err, cudaStream_t stream);
+cudaError_t launch_append_path(const void* k_draft, const void* v_draft, const int32_t* path, const int32_t* n_path,
+                               int32_t* taken, int T, void* res_k, void* res_v, int32_t* res_len, int batch, int Hkv,
+                               int P, int32_t* err, cudaStream_t stream);
+cudaError_t launch_select_pages(const SelectParams& p, int P, int dtype, cudaStream_t stream);
+cudaError_t launch_tree(const TreeParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_flush_commit(int32_t* res_len, const int32_t* new_page, int32_t* page_table, int max_pages,
                                 int32_t* num_pages, long long pool_pages, int batch, int P, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams& p, int gqa, int dtype, cudaStream_t stream);

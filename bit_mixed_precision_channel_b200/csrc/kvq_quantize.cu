@@ -688,6 +688,41 @@ __global__ void __launch_bounds__(256) append_kernel(const uint4* k_new, const u
   if (threadIdx.x == 0) res_len[b] = r + 1;
 }
 
+// The accepted path of a drafted tree: tokens path[b][taken[b] ..] of k_draft / v_draft into
+// the window, as many as it has room for, then res_len[b] and taken[b] advance by that many.
+// One CTA per sequence, so that every thread has read the lengths before they change.
+__global__ void __launch_bounds__(512) append_path_kernel(const uint4* k_draft, const uint4* v_draft,
+                                                          const int32_t* path, const int32_t* n_path, int32_t* taken,
+                                                          int T, uint4* res_k, uint4* res_v, int32_t* res_len, int Hkv,
+                                                          int P, int32_t* err) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x;
+  const int r = res_len[b], t0 = taken[b], n = n_path[b];
+  if (r < 0 || r > P || n < 0 || n > T || t0 < 0 || t0 > n) {
+    if (threadIdx.x == 0) flag_error(err, KVQ_DEV_ERR_LENGTH);
+    return;
+  }
+  const int m = min(n - t0, P - r);
+  for (int i = threadIdx.x; i < m * Hkv * 16; i += blockDim.x) {
+    const int s = i / (Hkv * 16), j = i - s * (Hkv * 16), h = j >> 4, c = j & 15;
+    int node = path[size_t(b) * T + t0 + s];
+    if (node < 0 || node >= T) {
+      flag_error(err, KVQ_DEV_ERR_LENGTH);
+      node = 0;
+    }
+    const size_t src = (size_t(b) * T + node) * Hkv * 16 + j;
+    const size_t dst = ((size_t(b) * Hkv + h) * P + r + s) * 16 + c;
+    res_k[dst] = k_draft[src];
+    res_v[dst] = v_draft[src];
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && m > 0) {
+    res_len[b] = r + m;
+    taken[b] = t0 + m;
+  }
+}
+
 // a5 (second half): after the full windows were quantized into their new pages, link
 // the pages and empty the windows.  Uses the same predicate as the quantize launch, so a
 // sequence skipped there (bad page id, full table) is skipped here too.
@@ -742,6 +777,15 @@ cudaError_t launch_append(const void* k_new, const void* v_new, void* res_k, voi
   return launch_pdl(append_kernel, dim3(batch), dim3(256), 0, stream, static_cast<const uint4*>(k_new),
                     static_cast<const uint4*>(v_new), static_cast<uint4*>(res_k), static_cast<uint4*>(res_v), res_len,
                     Hkv, P, err);
+}
+
+cudaError_t launch_append_path(const void* k_draft, const void* v_draft, const int32_t* path, const int32_t* n_path,
+                               int32_t* taken, int T, void* res_k, void* res_v, int32_t* res_len, int batch, int Hkv,
+                               int P, int32_t* err, cudaStream_t stream) {
+  if (batch <= 0) return cudaSuccess;
+  return launch_pdl(append_path_kernel, dim3(batch), dim3(512), 0, stream, static_cast<const uint4*>(k_draft),
+                    static_cast<const uint4*>(v_draft), path, n_path, taken, T, static_cast<uint4*>(res_k),
+                    static_cast<uint4*>(res_v), res_len, Hkv, P, err);
 }
 
 cudaError_t launch_flush_commit(int32_t* res_len, const int32_t* new_page, int32_t* page_table, int max_pages,

@@ -382,6 +382,95 @@ KVQ_API kvq_status kvq_gather_tokens(const kvq_config* cfg, const void* k, const
                                      const int32_t* keep, int32_t n, void* k_out, void* v_out,
                                      int32_t* err, cudaStream_t stream);
 
+/* ---- Speculative decoding on the quantized cache ----
+ * A step drafts a few tokens with attention over few pages (kvq_select_pages,
+ * kvq_decode_attention_sparse), verifies the drafted tree in one pass over all of them
+ * (kvq_tree_attention) and keeps the accepted path (kvq_append_path).  (The pages on the
+ * method have no counterpart of these calls.) */
+
+/* Choice of the pages a decode step reads.  For every sequence b and KV head h the pages
+ * of page_table[b] are scored by the largest logits their stored key ranges allow, and
+ * n_sel[b] = min(n_select, num_pages[b]) of them are chosen: the first n_first and the
+ * last n_recent pages always, the others by score, ties going to the lower slot.
+ *   score(page) = max over its 32-token groups of
+ *       sum_c pos_c * (z_c + 3 * sA_c) + sum_j pos_idx(j) * 3 * sB_j + sum_c neg_c * z_c,
+ *   pos_c = sum over the query heads of h of max(q_c, 0), neg_c = the same of min(q_c, 0),
+ * sA, z, sB and idx the record's plane-A scale and zero point, plane-B scale and boosted
+ * channels: no token of the group can give the heads a larger sum of q . k.  The scores
+ * are carried in 64 bits, so the choice does not depend on the order of summation.
+ * q: dtype [batch][Hq][D].  sel: int32 [batch][Hkv][n_select], written with the chosen
+ * slots (positions in page_table[b], not page ids) in ascending order, then -1; n_sel:
+ * int32 [batch].  A sequence with at most n_select pages keeps them all and is not scored.
+ * Requires n_select >= 1, n_first + n_recent <= n_select and max_pages <= 204800
+ * (KVQ_ERR_UNSUPPORTED above).  An invalid num_pages[b] sets KVQ_DEV_ERR_LENGTH and chooses
+ * nothing for b; a query that is not finite sets KVQ_DEV_ERR_RANGE.  One launch, no
+ * workspace; calls may overlap on the GPU if they write different sel and n_sel. */
+KVQ_API kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
+                                    int32_t batch, const int32_t* page_table, int32_t max_pages,
+                                    const int32_t* num_pages, int32_t n_first, int32_t n_recent,
+                                    int32_t n_select, int32_t* sel, int32_t* n_sel, int32_t* err,
+                                    cudaStream_t stream);
+
+/* kvq_decode_attention over chosen pages: for every sequence b and query head h of KV head
+ * kh, attention over the pages in slots sel[b][kh][0 .. n_sel[b]) of page_table[b], followed
+ * by the res_len[b] residual tokens.  sel: int32 [batch][Hkv][max_sel], as kvq_select_pages
+ * writes it (or any other choice, in any order; a slot listed twice counts twice).  A slot
+ * outside [0, num_pages[b]) sets KVQ_DEV_ERR_PAGE_RANGE, n_sel[b] outside [0, max_sel]
+ * KVQ_DEV_ERR_LENGTH.  Everything else (q, out, workspace of
+ * kvq_decode_workspace_bytes(cfg, batch, max_pages) bytes with its zero-counter contract,
+ * precision, empty sequences, errors) as for kvq_decode_attention, on the same kernel. */
+KVQ_API kvq_status kvq_decode_attention_sparse(const kvq_config* cfg, const void* pool, int64_t pool_pages,
+                                               const void* q, int32_t batch, const int32_t* page_table,
+                                               int32_t max_pages, const int32_t* num_pages, const int32_t* sel,
+                                               int32_t max_sel, const int32_t* n_sel, const void* res_k,
+                                               const void* res_v, const int32_t* res_len, float sm_scale,
+                                               float* out, void* workspace, size_t workspace_bytes, int32_t* err,
+                                               cudaStream_t stream);
+
+/* Most drafted tokens of a sequence. */
+#define KVQ_MAX_DRAFT 128
+
+/* Scratch bytes of kvq_tree_attention on the current device, 0 for arguments it rejects.
+ * The contents need no preparation and carry nothing from call to call; calls that may
+ * overlap on the GPU need a workspace each. */
+KVQ_API size_t kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n_draft);
+
+/* Attention of a tree of drafted tokens over the cache: for every sequence b, drafted token
+ * i < draft_len[b] and query head h (KV head h / (Hq/Hkv)),
+ *   out[b][i][h] = softmax(sm_scale * q[b][i][h] . K^T) V
+ * over the num_pages[b] quantized pages, the res_len[b] residual tokens and the drafted
+ * tokens j < draft_len[b] whose bit is set in the mask of i: bit j % 32 of
+ * mask[b][i][j / 32].  A tree sets the bits of the ancestors of i and of i itself, a chain
+ * those of j <= i; any other mask is taken as it stands.  n_draft = 1 is the single-token
+ * decode step before its token is appended.
+ * q: dtype [batch][n_draft][Hq][D]; k_draft, v_draft: dtype [batch][n_draft][Hkv][D]; mask:
+ * uint32 [batch][n_draft][ceil(n_draft / 32)]; draft_len: int32 [batch], each in
+ * [0, n_draft]; out: fp32 [batch][n_draft][Hq][D], 16-byte aligned.  1 <= n_draft <=
+ * KVQ_MAX_DRAFT (KVQ_ERR_UNSUPPORTED above).  Rows i >= draft_len[b] of out are left as they
+ * were, and nothing of the drafted tokens behind draft_len[b] or of window rows behind
+ * res_len[b] takes part, whatever it holds.  A row that sees no token at all is zero.
+ * Invalid lengths set KVQ_DEV_ERR_LENGTH, and the sequence's rows are left as they were. */
+KVQ_API kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
+                                      int32_t n_draft, int32_t batch, const int32_t* page_table,
+                                      int32_t max_pages, const int32_t* num_pages, const void* res_k,
+                                      const void* res_v, const int32_t* res_len, const void* k_draft,
+                                      const void* v_draft, const uint32_t* mask, const int32_t* draft_len,
+                                      float sm_scale, float* out, void* workspace, size_t workspace_bytes,
+                                      int32_t* err, cudaStream_t stream);
+
+/* The accepted path of a drafted tree into the residual window: tokens path[b][taken[b]],
+ * path[b][taken[b] + 1], ... path[b][n_path[b] - 1] of k_draft / v_draft (dtype
+ * [batch][n_draft][Hkv][D]) are written behind the res_len[b] tokens of the window, as many
+ * as it has room for; res_len[b] and taken[b] advance by that number.  A path that does not
+ * fit is finished by kvq_flush_residual and a second call; taken starts at zero, and is
+ * n_path[b] when the path is in the cache.  path: int32 [batch][n_draft]; n_path, taken:
+ * int32 [batch].  A length outside its range sets KVQ_DEV_ERR_LENGTH and skips the sequence;
+ * a path entry outside [0, n_draft) sets KVQ_DEV_ERR_LENGTH and copies token 0. */
+KVQ_API kvq_status kvq_append_path(const kvq_config* cfg, int32_t batch, int32_t n_draft, const void* k_draft,
+                                   const void* v_draft, const int32_t* path, const int32_t* n_path,
+                                   int32_t* taken, void* res_k, void* res_v, int32_t* res_len, int32_t* err,
+                                   cudaStream_t stream);
+
 /* Bytes of one (page, KV head) record of a dense cache: K rows then V rows, dtype
  * [2][page_tokens][head_dim]; 0 if cfg is not supported. */
 KVQ_API size_t kvq_dense_page_bytes(const kvq_config* cfg);
