@@ -430,7 +430,7 @@ kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int64_t poo
 
 size_t kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n_draft) {
   if (kvq_check_config(cfg) != KVQ_OK || batch < 0 || n_draft < 1 || n_draft > KVQ_MAX_DRAFT) return 0;
-  return 256;
+  return size_t(2) * sm_count() * 128 * (kHeadDim + 4) * sizeof(float);
 }
 
 kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
@@ -447,7 +447,11 @@ kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t p
   if (batch == 0) return KVQ_OK;
   if (!k_draft || !v_draft || !mask || !draft_len || !workspace) return KVQ_ERR_INVALID_ARG;
   if (!aligned16(k_draft) || !aligned16(v_draft) || !aligned16(out) || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
-  if (batch > 65535 || cfg->num_q_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  // the tiles of the work line are numbered with 32 bits
+  const long long gq = cfg->num_q_heads / cfg->num_kv_heads;
+  if ((long long)batch * cfg->num_kv_heads * ((n_draft * gq + 127) / 128) *
+          (((long long)max_pages * cfg->page_tokens + 127) / 128 + 2) >= (1ll << 31))
+    return KVQ_ERR_INVALID_ARG;
   if (workspace_bytes < kvq_tree_workspace_bytes(cfg, batch, n_draft)) return KVQ_ERR_CAPACITY;
   TreeParams p{};
   p.pool = static_cast<const uint8_t*>(pool);
@@ -474,6 +478,8 @@ kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t p
   p.draft_len = draft_len;
   p.c_log2 = sm_scale * 1.4426950408889634f;
   p.out = out;
+  p.part = static_cast<float*>(workspace);
+  p.n_ctas = sm_count();
   p.err = err;
   return cuda_status(launch_tree(p, cfg->dtype, stream));
 }

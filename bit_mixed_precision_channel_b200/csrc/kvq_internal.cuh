@@ -387,6 +387,8 @@ struct TreeParams {
   const int32_t* draft_len;
   float c_log2;
   float* out;  // [batch][T][Hq][128]
+  float* part;  // [2 * n_ctas][128][132]: rows of units cut by a range boundary
+  int n_ctas;   // grid size: one CTA per SM
   int32_t* err;
 };
 

@@ -1,0 +1,1061 @@
+// kvq_tree_impl.cuh — attention of a tree of drafted tokens over the paged 2-bit cache on
+// the fifth-generation tensor cores (sm_100a).  Kernel templates; kvq_tree_<dtype>.cu
+// instantiate them, kvq_tree.cu holds the host side.
+//
+// Row (i, head) of sequence b, drafted token i < draft_len[b], attends to every token of
+// the quantized pages and of the residual window, and to the drafted tokens j that bit j of
+// its mask names:  out = sum_t p_t v_t / sum_t p_t,  p_t = 2^(c q . k_t - M).
+//
+// Work.  A unit is (sequence, kv head, 128 rows); its items are tiles of 128 tokens: the
+// pages' (128 / P pages each), then the window and the drafted tokens end to end as raw
+// tiles.  The units' tiles are laid end to end and cut into one equal range per SM.  A CTA
+// that holds a whole unit writes its rows; the parts of a unit that was cut go to the
+// workspace, and merge_kernel joins them.
+//
+// Per tile, with thread roles that run ahead of one another through mbarriers:
+//   producer   1 warp    copies the page records (one bulk copy each, three tiles ahead);
+//   dequant    8 warps   writes the keys and the value codes as fp16 operands;
+//   issuer     1 thread  S = Q K^T, then O += P V of the tile before (tcgen05, M = 128);
+//   softmax    8 warps   a thread per (row, half of the tile's tokens): S from tensor
+//                        memory, running maximum, P back over S.
+// Two S / P buffers of 144 columns, O (128 columns) and Q (64 columns) fill tensor memory.
+//
+// Arithmetic.  Everything is carried to about 22 bits, as the decode kernel does, so that a
+// drafted token verified here sees the logits that the decode step would give it:
+//  * a key is u * s + z with u = codeA + codeB / 4 (plane-A scale = 4 x plane-B scale).
+//    The fp16 product u * s / 2 is split exactly into its rounding and the remainder (one
+//    HMUL2, one HFMA2 for two elements): two operand tiles.  The zero points depend on the
+//    32-token group alone, so they are 4 more rows of the key operand, and q . z comes out
+//    in columns 128..131 of S;
+//  * the query enters as q * 2^-e (exact), e from its largest element;
+//  * the value scale is folded into the probability, P = p * sV as a high and a low fp16
+//    part, so the value operand is the 2-bit codes themselves; sum p z is added in fp32.
+//    The running reference M covers the largest p * sV of a tile, so P stays inside fp16
+//    whatever the value scales are;
+//  * window and drafted tokens go through the same products: K / 2 and V * 2^-e_t in fp16,
+//    with 2^e_t (bf16 only; the token's largest value) in the place of the value scale.
+#pragma once
+#include <type_traits>
+
+#include "kvq_internal.cuh"
+#include "kvq_tc.cuh"
+
+namespace kvq {
+namespace tree {
+
+constexpr int kSoftWarps = 8, kDeqWarps = 8;
+constexpr int kIssuer = kSoftWarps + kDeqWarps, kProducer = kIssuer + 1;
+constexpr int kThreads = 640;  // 5 warpgroups: two of softmax, two of dequant, one with the issuer and the producer
+// Registers a thread: at launch, then by role (setmaxnreg): 2 x 128 + 2 x 80 + 64 = 5 x 96,
+// so the split draws on exactly what the block was launched with.
+constexpr int kRegsLaunch = 96, kRegsSoft = 128, kRegsDeq = 80, kRegsRest = 64;
+static_assert(2 * kRegsSoft + 2 * kRegsDeq + kRegsRest <= 5 * kRegsLaunch, "register split");
+constexpr int kRecStages = 3;
+// The tensor cores round their fp32 accumulator toward zero: 16 products a tile shrink a long
+// sum by about 2^-24 each.  O is therefore moved every kFlush tiles into fp32 sums in shared
+// memory, which round to nearest.  (Left in tensor memory over 28 tiles of a 4096-token
+// cache, the output was off by 3.6e-5 against 64 bits.)
+constexpr int kFlush = 4;
+// shared-memory offsets: key operand (high parts and zero points, remainders), value operand,
+// output sums, record stages
+constexpr uint32_t kKhi = 0, kKlo = 144 * 256, kV = kKlo + 128 * 256, kAcc = kV + 128 * 256, kRec = kAcc + 128 * 512;
+constexpr int kColS = 144, kColO = 288, kColQ = 416;  // tensor-memory columns: S at 0 and 144
+
+__device__ __forceinline__ uint32_t tco(int r, int c) { return uint32_t((r >> 3) * 2048 + c * 128 + (r & 7) * 16); }
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// True in one lane of a converged warp.  The tensor-core products are issued under it by a
+// warp whose lanes all walk the same loop: the operands then sit in uniform registers, and a
+// product of N = 128 columns takes 64 cycles; issued under `if (lane == 0)`, where each
+// operand is moved there first, it took 150 to 220 whatever its size (measured).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(x));
+  return x != 0;
+}
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }  // e in [-126, 127]
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint32_t u, __half) { return __half22float2(u32_as_h2(u)); }
+__device__ __forceinline__ float2 unpack2(uint32_t u, __nv_bfloat16) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+// Two scales or zero points as fp16 (bf16: exact inside fp16's normal range).
+__device__ __forceinline__ uint32_t meta_h2(uint32_t x, __half) { return x; }
+__device__ __forceinline__ uint32_t meta_h2(uint32_t x, __nv_bfloat16) {
+  const float2 f = unpack2(x, __nv_bfloat16());
+  return pack_h2(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t half_of(uint32_t x) {  // x / 2 of an fp16 pair
+  return h2_as_u32(__hmul2(u32_as_h2(x), __float2half2_rn(0.5f)));
+}
+
+// Tiles of one unit of sequence b; 0 units for invalid lengths or no drafted token.
+struct Seq {
+  int np, rl, dl;
+  int ntp, nt, nrt;  // page tiles, tiles, row tiles
+};
+__device__ __forceinline__ bool seq_load(const TreeParams& p, int b, Seq& s) {
+  s.np = __ldcg(p.num_pages + b);
+  s.rl = __ldcg(p.res_len + b);
+  s.dl = __ldcg(p.draft_len + b);
+  const bool ok = s.np >= 0 && s.np <= p.max_pages && s.rl >= 0 && s.rl <= p.P && s.dl >= 0 && s.dl <= p.T;
+  if (!ok) s.np = s.rl = s.dl = 0;
+  s.ntp = (s.np * p.P + 127) / 128;
+  s.nt = s.ntp + (s.rl + s.dl + 127) / 128;
+  s.nrt = (s.dl * p.gqa + 127) / 128;
+  return ok;
+}
+__device__ __forceinline__ int seq_tiles(const TreeParams& p, const Seq& s) { return s.nrt * s.nt * p.Hkv; }
+
+// A walk over the tiles [pos, end) of the line.
+struct Walk {
+  Seq s;
+  int b, h, r, k;  // sequence, kv head, row tile, tile of the unit
+  int pos, end;
+  bool first, last;  // of this CTA's part of the unit
+  __device__ __forceinline__ void start(const TreeParams& p, int b0, int base, int from, int to) {
+    b = b0;
+    seq_load(p, b, s);
+    const int off = from - base, u = off / s.nt;
+    k = off - u * s.nt;
+    h = u / s.nrt;
+    r = u - h * s.nrt;
+    pos = from;
+    end = to;
+    first = true;
+    last = k == s.nt - 1 || pos == end - 1;
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p) {
+    if (++pos >= end) return false;
+    first = false;
+    if (++k == s.nt) {
+      k = 0;
+      first = true;
+      if (++r == s.nrt) {
+        r = 0;
+        if (++h == p.Hkv) {
+          h = 0;
+          do {
+            ++b;
+            seq_load(p, b, s);
+          } while (s.nrt == 0 && b < p.batch - 1);
+        }
+      }
+    }
+    last = k == s.nt - 1 || pos == end - 1;
+    return true;
+  }
+  __device__ __forceinline__ bool raw() const { return k >= s.ntp; }
+};
+
+// Range of CTA i of n over W tiles, and the CTA whose range holds tile x.
+__device__ __forceinline__ int range_at(int i, int W, int n) { return int((long long)W * i / n); }
+__device__ __forceinline__ int range_owner(int x, int W, int n) { return int(((long long)(x + 1) * n - 1) / W); }
+
+// Total tiles of the line, and the sequence (with its first tile) that holds tile range_at(
+// cta): every thread of a block of NT threads takes part.
+struct Line {
+  int W, n, b0, base0;
+  int sums[32];
+};
+template <int NT>
+__device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta, int ctas, bool flag) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int run = 0, at = 0;
+    if (pass == 1) {
+      if (tid == 0) {
+        ln.W = total;
+        ln.n = min(ctas, total);
+      }
+      if (cta >= min(ctas, total)) break;
+      at = range_at(cta, total, min(ctas, total));
+    }
+    for (int base = 0; base < p.batch; base += NT) {
+      const int b = base + tid;
+      int x = 0;
+      if (b < p.batch) {
+        Seq s;
+        if (!seq_load(p, b, s) && flag && pass == 0) flag_error(p.err, KVQ_DEV_ERR_LENGTH);
+        x = seq_tiles(p, s);
+      }
+      int incl = x;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, off);
+        if (lane >= off) incl += y;
+      }
+      if (lane == 31) ln.sums[warp] = incl;
+      __syncthreads();
+      int before = run, all = 0;
+      for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += ln.sums[w];
+        all += ln.sums[w];
+      }
+      run += all;
+      if (pass == 1 && x > 0 && before + incl - x <= at && at < before + incl) {
+        ln.b0 = b;
+        ln.base0 = before + incl - x;
+      }
+      __syncthreads();
+    }
+    total = run;
+  }
+  __syncthreads();
+}
+
+struct Shared {
+  uint64_t rec_full[kRecStages], rec_empty[kRecStages], k_full, k_empty, v_full, v_empty, s_full[2], p_full[2], pv_done[2],
+      q_full;
+  uint32_t tmem;
+  int abort;
+  float xch[2][128][2];                 // [parity][row][half]
+  __align__(16) float vs[3][128];       // value scale (raw tiles: 2^e_t / 2) of a tile's tokens
+  __align__(16) float vz[3][128];       // value zero point
+  float smax[3][4];                     // largest value scale of a page tile's groups
+  float xs[3][kDeqWarps];               // the same of a raw tile, by the warp that wrote it
+  __align__(16) uint2 tab[kDeqWarps][4][34];  // moves of boosted codes: {rotation | source word << 8, mask} per word
+  Line line;
+};
+
+// Waits for a phase; false once any wait of the CTA has given up.
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, int32_t* err) {
+  if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
+  if (mbar_wait_bounded(bar, parity)) return true;
+  flag_error(err, KVQ_DEV_ERR_TIMEOUT);
+  *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+  return false;
+}
+
+// The same by a whole warp, with one answer for all lanes.
+__device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t parity, int32_t* err) {
+  return __all_sync(kFull, wait(sh, bar, parity, err));
+}
+
+constexpr int kPart = 132;  // floats of a partial row: unnormalised output, reference M, sum
+
+// ---------------------------------------------------------------- dequantization
+
+// The boosted channels of a page whose plane-A code sits in an odd (half = 1) or even word:
+// for each of the four words q (word 2q + half), the rotation that brings the plane-B code
+// of row j to its channel's bits.  Lists are padded to an even length; counts in n[4].
+template <int KB>
+__device__ __forceinline__ void boost_moves(const uint8_t* idx, int half, uint2 (*tab)[34], int (&n)[4], int lane) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) n[q] = 0;
+#pragma unroll
+  for (int j0 = 0; j0 < 16 * KB; j0 += 32) {
+    const int j = j0 + lane;
+    int dq = -1;
+    uint2 m = make_uint2(0u, 0u);
+    if (j < 16 * KB) {
+      const int src = boost_pos(j, KB), dst = key_pos(idx[j] & 127);
+      if (((dst >> 4) & 1) == half) dq = dst >> 5;
+      const int sb = elem_bit(src & 15), db = elem_bit(dst & 15);
+      m = make_uint2(uint32_t((sb - db) & 31) | (uint32_t(src >> 4) << 8), 3u << db);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t bal = __ballot_sync(kFull, dq == q);
+      if (dq == q) tab[q][min(n[q] + __popc(bal & ((1u << lane) - 1u)), 32)] = m;
+      n[q] += __popc(bal);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    n[q] = min(n[q], 32);  // 16 channels a word; more only in a record that repeats an index
+    if (lane == 0 && (n[q] & 1)) tab[q][n[q]] = make_uint2(0u, 0u);
+  }
+  __syncwarp();
+}
+
+// Keys of token `row` of the tile (token tp of the page record), the 64 channels of `half`.
+template <typename T, int KB>
+__device__ __forceinline__ void key_row(const TreeParams& p, const uint8_t* rec, int tp, int row, int half, uint8_t* smem,
+                                        const uint2 (*tab)[34], const int (&n)[4]) {
+  const uint4 w0 = lds128(rec + p.L.k_codes + tp * 32), w1 = lds128(rec + p.L.k_codes + tp * 32 + 16);
+  const uint32_t w[4] = {half ? w0.y : w0.x, half ? w0.w : w0.z, half ? w1.y : w1.x, half ? w1.w : w1.z};
+  uint32_t wb[4] = {0u, 0u, 0u, 0u};
+  if constexpr (KB == 8) {  // every channel boosted: plane B has the layout of plane A
+    const uint4 b0 = lds128(rec + p.L.kb_codes + tp * 32), b1 = lds128(rec + p.L.kb_codes + tp * 32 + 16);
+    wb[0] = half ? b0.y : b0.x;
+    wb[1] = half ? b0.w : b0.z;
+    wb[2] = half ? b1.y : b1.x;
+    wb[3] = half ? b1.w : b1.z;
+  } else if constexpr (KB > 0) {
+    const uint8_t* brow = rec + p.L.kb_codes + tp * (4 * KB);
+    uint32_t src0 = 0u, src1 = 0u;
+    if constexpr (KB <= 2) {
+      src0 = lds32(brow);
+      if constexpr (KB == 2) src1 = lds32(brow + 4);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t acc = 0u;
+      for (int e = 0; e < n[q]; e += 2) {
+        const uint4 m = *reinterpret_cast<const uint4*>(&tab[q][e]);
+        uint32_t a, b;
+        if constexpr (KB == 1) {
+          a = b = src0;
+        } else if constexpr (KB == 2) {
+          a = (m.x >> 8) ? src1 : src0;
+          b = (m.z >> 8) ? src1 : src0;
+        } else {
+          a = lds32(brow + 4 * (m.x >> 8));
+          b = lds32(brow + 4 * (m.z >> 8));
+        }
+        acc |= (__funnelshift_r(a, a, m.x) & m.y) | (__funnelshift_r(b, b, m.z) & m.w);
+      }
+      wb[q] = acc;
+    }
+  }
+  const int gp = tp >> 5;
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    uint32_t hi[4][4], lo[4][4];  // [word q][k-step bit, 8-channel bit]
+    const uint8_t* sc = rec + p.L.k_scale + gp * 256 + 64 * (2 * half + a);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t u[4];
+      e2m1_pairs(code_pass(w[q], a), u[0], u[1], u[2], u[3]);
+      if constexpr (KB > 0) {
+        uint32_t ub[4];
+        e2m1_pairs(code_pass(wb[q], a), ub[0], ub[1], ub[2], ub[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          u[i] = h2_as_u32(__hfma2(u32_as_h2(ub[i]), __float2half2_rn(0.25f), u32_as_h2(u[i])));
+      }
+      const uint4 s4 = lds128(sc + 16 * q);
+      const uint32_t s[4] = {meta_h2(s4.x, T()), meta_h2(s4.y, T()), meta_h2(s4.z, T()), meta_h2(s4.w, T())};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 x = __hmul2(u32_as_h2(u[i]), u32_as_h2(s[i]));
+        hi[q][i] = h2_as_u32(x);
+        lo[q][i] = h2_as_u32(__hfma2(u32_as_h2(u[i]), u32_as_h2(s[i]), __hneg2(x)));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t at = tco(row, 8 * half + 4 * a + i);
+      *reinterpret_cast<uint4*>(smem + kKhi + at) = make_uint4(hi[0][i], hi[1][i], hi[2][i], hi[3][i]);
+      *reinterpret_cast<uint4*>(smem + kKlo + at) = make_uint4(lo[0][i], lo[1][i], lo[2][i], lo[3][i]);
+    }
+  }
+}
+
+// Value codes of group g of the tile (group gp of the page record): channels of m-tiles
+// 4 mh .. 4 mh + 3, tokens contiguous (K-major operand of the second product).
+__device__ __forceinline__ void value_codes(const TreeParams& p, const uint8_t* rec, int gp, int g, int mh, uint8_t* smem,
+                                            int lane) {
+  const int w = lane & 7, m3 = lane >> 3, m = 4 * mh + m3;
+  const uint8_t* vq = rec + p.L.v_codes + (((2 * gp + mh) * 32 + 4 * w) * 4 + m3) * 4;
+  uint32_t x[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) x[q] = lds32(vq + 16 * q);
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    uint32_t u[4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) e2m1_pairs(code_pass(x[q], a), u[q][0], u[q][1], u[q][2], u[q][3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // byte 2u + v: tokens 8u.., channels 8v..
+      *reinterpret_cast<uint4*>(smem + kV + (2 * m + (i & 1)) * 2048 + (4 * g + 2 * a + (i >> 1)) * 128 + w * 16) =
+          make_uint4(u[0][i], u[1][i], u[2][i], u[3][i]);
+  }
+}
+
+// Window and drafted tokens: source row of token x of the raw sequence.
+__device__ __forceinline__ size_t raw_row(const TreeParams& p, int b, int h, int rl, int x, bool& draft) {
+  draft = x >= rl;
+  return draft ? ((size_t(b) * p.T + (x - rl)) * p.Hkv + h) * 16 : ((size_t(b) * p.Hkv + h) * p.P + x) * 16;
+}
+
+// Whether any row sees drafted token j.
+static __device__ __noinline__ bool seen_by_any(const TreeParams& p, int b, int dl, int j) {
+  for (int i = 0; i < dl; ++i)
+    if ((__ldcg(p.mask + (size_t(b) * p.T + i) * p.W + (j >> 5)) >> (j & 31)) & 1u) return true;
+  return false;
+}
+
+// An fp16 pair / bf16 pair with the elements that are no finite number set to zero.
+__device__ __forceinline__ uint32_t finite2(uint32_t x, uint32_t expo, bool& bad) {
+  const bool a = (x & expo) == expo, b = (x & (expo << 16)) == (expo << 16);
+  bad |= a | b;
+  return (a ? 0u : x & 0xffffu) | (b ? 0u : x & 0xffff0000u);
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <typename T, int KB>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+  constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (warp == kIssuer) tc::alloc(&sh.tmem, 512);
+  if (tid == 0) {
+    for (int i = 0; i < kRecStages; ++i) {
+      mbar_init(&sh.rec_full[i], 1);
+      mbar_init(&sh.rec_empty[i], kDeqWarps);
+    }
+    mbar_init(&sh.k_full, kDeqWarps);
+    mbar_init(&sh.k_empty, 1);
+    mbar_init(&sh.v_full, kDeqWarps);
+    mbar_init(&sh.v_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], kSoftWarps);
+      mbar_init(&sh.pv_done[i], 1);
+    }
+    mbar_init(&sh.q_full, kSoftWarps);
+    fence_mbar_init();
+    sh.abort = 0;
+  }
+  // a probability of zero meets whatever the value operand holds: start from finite contents
+  for (int i = tid; i < int((kAcc - kV) / 16); i += kThreads)
+    reinterpret_cast<uint4*>(smem + kV)[i] = make_uint4(0u, 0u, 0u, 0u);
+  pdl_wait();
+  line_find<kThreads>(p, sh.line, blockIdx.x, p.n_ctas, blockIdx.x == 0);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = sh.tmem;
+  const int W = sh.line.W, n_ctas = sh.line.n, cta = blockIdx.x;
+  const bool idle = cta >= n_ctas;
+  Walk wk;
+  if (!idle) wk.start(p, sh.line.b0, sh.line.base0, range_at(cta, W, n_ctas), range_at(cta + 1, W, n_ctas));
+  const int PPT = 128 / p.P;  // pages of a tile
+  const uint32_t stage_bytes = uint32_t(PPT) * p.L.record;
+
+  if (idle) {
+    // nothing to do
+  } else if (warp >= kIssuer) {
+    regs_dec<kRegsRest>();
+    if (warp == kProducer) {
+    // ------------------------------------------------------------ producer
+    const uint64_t policy = l2_evict_first_policy();
+    int n = 0;
+    bool more = true;
+    while (more) {
+      if (!wk.raw()) {
+        const int st = n % kRecStages, npg = min(PPT, wk.s.np - wk.k * PPT);
+        int id = 0;
+        if (lane < npg) {
+          id = __ldcg(p.page_table + size_t(wk.b) * p.max_pages + wk.k * PPT + lane);
+          if (id < 0 || id >= p.pool_pages) {
+            flag_error(p.err, KVQ_DEV_ERR_PAGE_RANGE);
+            id = 0;
+          }
+        }
+        if (n >= kRecStages && !wait_warp(sh, &sh.rec_empty[st], uint32_t(n / kRecStages - 1) & 1u, p.err)) break;
+        if (lane == 0) {
+          tc::fence_async_smem();
+          mbar_arrive_expect_tx(&sh.rec_full[st], uint32_t(npg) * p.L.payload);
+        }
+        __syncwarp();
+        if (lane < npg)
+          bulk_g2s(smem + kRec + st * stage_bytes + lane * p.L.record, p.pool + (size_t(id) * p.Hkv + wk.h) * p.L.record,
+                   p.L.payload, &sh.rec_full[st], policy);
+        ++n;
+      }
+      more = wk.next(p);
+    }
+    // every copy has landed before the shared memory is released
+    __syncwarp();
+    if (lane == 0)
+      for (int y = max(0, n - kRecStages); y < n; ++y)
+        mbar_wait_bounded(&sh.rec_full[y % kRecStages], uint32_t(y / kRecStages) & 1u);
+    } else if (warp == kIssuer) {
+    // ------------------------------------------------------------ issuer
+    const uint32_t sKh = smem_addr(smem + kKhi), sKl = smem_addr(smem + kKlo), sV = smem_addr(smem + kV);
+    constexpr uint32_t kIdHi = tc::idesc_f16(144, false, false), kIdLo = tc::idesc_f16(128, false, false),
+                       kIdMn = tc::idesc_f16(128, false, true);
+    int it = 0, seg = 0;
+    bool more = true, ok = true;
+    bool praw = false, pfresh = false;  // the tile before: raw; O starts anew with it
+    auto second = [&](int j) {          // O += P V of tile j
+      const uint32_t tP = tm + uint32_t(j & 1) * kColS;
+      ok = ok && wait_warp(sh, &sh.p_full[j & 1], uint32_t(j >> 1) & 1u, p.err) &&
+           wait_warp(sh, &sh.v_full, uint32_t(j) & 1u, p.err);
+      if (!ok) return;
+      tc::fence_after();
+      if (elect_one()) {
+        if (praw) {
+#pragma unroll
+          for (int s = 0; s < 16; ++s)
+            tc::mma(tm + kColO, tP + 8 * s, tc::smem_desc(sV + (s & 7) * 4096, 2048, 128), kIdMn, s > 0 || !pfresh);
+        } else {
+#pragma unroll
+          for (int s = 0; s < 16; ++s)
+            tc::mma(tm + kColO, tP + 8 * s, tc::smem_desc(sV + (s & 7) * 256, 128, 2048), kIdLo, s > 0 || !pfresh);
+        }
+        tc::commit(&sh.v_empty);
+        tc::commit(&sh.pv_done[j & 1]);
+      }
+      __syncwarp();
+    };
+    int run = 0;  // tiles of this CTA's part of the unit so far
+    while (more && ok) {
+      if (wk.first) {
+        if (it > 0) second(it - 1);
+        ok = ok && wait_warp(sh, &sh.q_full, uint32_t(seg++) & 1u, p.err);
+        run = 0;
+      }
+      ok = ok && wait_warp(sh, &sh.k_full, uint32_t(it) & 1u, p.err);
+      if (!ok) break;
+      tc::fence_after();
+      const uint32_t dS = tm + uint32_t(it & 1) * kColS;
+      if (elect_one()) {
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          tc::mma(dS, tm + kColQ + 8 * s, tc::smem_desc(sKh + s * 256, 128, 2048), kIdHi, s > 0);
+        if (!wk.raw()) {
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            tc::mma(dS, tm + kColQ + 8 * s, tc::smem_desc(sKl + s * 256, 128, 2048), kIdLo, 1u);
+        }
+        tc::commit(&sh.k_empty);
+        tc::commit(&sh.s_full[it & 1]);
+      }
+      __syncwarp();
+      if (!wk.first) second(it - 1);
+      praw = wk.raw();
+      pfresh = run++ % kFlush == 0;
+      ++it;
+      more = wk.next(p);
+    }
+    if (ok) second(it - 1);
+    // the products have completed before the operands' memory is released
+    if (ok) wait_warp(sh, &sh.pv_done[(it - 1) & 1], uint32_t((it - 1) >> 1) & 1u, p.err);
+    }
+  } else if (warp >= kSoftWarps) {
+    // ------------------------------------------------------------ dequantization
+    regs_dec<kRegsDeq>();
+    const int dw = warp - kSoftWarps, g = dw >> 1, half = dw & 1;
+    int it = 0, n = 0;
+    bool more = true;
+    while (more) {
+      const int v3 = it % 3;
+      if (!wk.raw()) {
+        const int st = n % kRecStages;
+        if (!wait_warp(sh, &sh.rec_full[st], uint32_t(n / kRecStages) & 1u, p.err)) break;
+        const int npg = min(PPT, wk.s.np - wk.k * PPT), pg = 32 * g / p.P, gp = g - pg * (p.P / 32);
+        const bool have = pg < npg;
+        const uint8_t* rec = smem + kRec + st * stage_bytes + pg * p.L.record;
+        int nm[4] = {0, 0, 0, 0};
+        if constexpr (KB > 0 && KB < 8)
+          if (have) boost_moves<KB>(rec + p.L.boost_idx, half, sh.tab[dw], nm, lane);
+        if (it > 0 && !wait_warp(sh, &sh.k_empty, uint32_t(it - 1) & 1u, p.err)) break;
+        if (have) {
+          key_row<T, KB>(p, rec, 32 * gp + lane, 32 * g + lane, half, smem, sh.tab[dw], nm);
+          if (lane >= 16 && half == 0) {  // zero points: row 128 + g of the key operand
+            const int c = lane - 16, s = c >> 1, r = c & 1;
+            const uint8_t* z = rec + p.L.k_zero + gp * 256 + (32 * (s >> 1) + 4 * (s & 1) + 2 * r) * 2;
+            uint32_t x[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q] = half_of(meta_h2(lds32(z + 16 * q), T()));
+            *reinterpret_cast<uint4*>(smem + kKhi + tco(128 + g, c)) = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+        if (half == 0) {
+          float s = 0.0f, z = 0.0f;
+          if (have) {
+            const int at = 2 * value_meta_pos(32 * gp + lane);
+            s = bits_to_float(*reinterpret_cast<const uint16_t*>(rec + p.L.v_scale + at), T());
+            z = bits_to_float(*reinterpret_cast<const uint16_t*>(rec + p.L.v_zero + at), T());
+          }
+          sh.vs[v3][32 * g + lane] = s;
+          sh.vz[v3][32 * g + lane] = z;
+          const uint32_t mx = __reduce_max_sync(kFull, __float_as_uint(fabsf(s)));
+          if (lane == 0) sh.smax[v3][g] = __uint_as_float(mx);
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.k_full);
+        if (it > 0 && !wait_warp(sh, &sh.v_empty, uint32_t(it - 1) & 1u, p.err)) break;
+        if (have) value_codes(p, rec, gp, g, half, smem, lane);
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.v_full);
+          mbar_arrive(&sh.rec_empty[st]);
+        }
+        ++n;
+      } else {
+        // window and drafted tokens: warp dw takes tokens 16 dw .. 16 dw + 15 of the tile, two at a time
+        const int x0 = 128 * (wk.k - wk.s.ntp), nx = wk.s.rl + wk.s.dl, c = lane & 15;
+        uint4 kx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int x = x0 + 16 * dw + 2 * i + (lane >> 4);
+          kx[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (x < nx) {
+            bool draft;
+            const size_t at = raw_row(p, wk.b, wk.h, wk.s.rl, x, draft) + c;
+            kx[i] = __ldcg(reinterpret_cast<const uint4*>(draft ? p.k_draft : p.res_k) + at);
+          }
+        }
+        if (it > 0 && !wait_warp(sh, &sh.k_empty, uint32_t(it - 1) & 1u, p.err)) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t* k = reinterpret_cast<uint32_t*>(&kx[i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2(k[e], T());
+            k[e] = pack_h2(0.5f * f.x, 0.5f * f.y);
+          }
+          *reinterpret_cast<uint4*>(smem + kKhi + tco(16 * dw + 2 * i + (lane >> 4), c)) = kx[i];
+        }
+        // the values: finite, and for bf16 brought below 2 by a power of two of the token
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int x = x0 + 16 * dw + 2 * i + (lane >> 4);
+          kx[i] = make_uint4(0u, 0u, 0u, 0u);
+          bool draft = false, bad = false;
+          if (x < nx) {
+            const size_t at = raw_row(p, wk.b, wk.h, wk.s.rl, x, draft) + c;
+            kx[i] = __ldcg(reinterpret_cast<const uint4*>(draft ? p.v_draft : p.res_v) + at);
+          }
+          uint32_t* v = reinterpret_cast<uint32_t*>(&kx[i]);
+          float m = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = finite2(v[e], BF ? 0x7f80u : 0x7c00u, bad);
+            const float2 f = unpack2(v[e], T());
+            m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+          if (bad && (!draft || seen_by_any(p, wk.b, wk.s.dl, x - wk.s.rl))) flag_error(p.err, KVQ_DEV_ERR_RANGE);
+          float s = 0.5f;
+          if constexpr (BF) {
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+            const int e = max(-100, min(100, int((__float_as_uint(m) >> 23) & 0xff) - 127));
+            const float f = pow2i(-e);
+            s = 0.5f * pow2i(e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 y = unpack2(v[j], T());
+              v[j] = pack_h2(y.x * f, y.y * f);
+            }
+          }
+          if (x >= nx) s = 0.0f;
+          if (c == 0) {
+            sh.vs[v3][16 * dw + 2 * i + (lane >> 4)] = s;
+            sh.vz[v3][16 * dw + 2 * i + (lane >> 4)] = 0.0f;
+          }
+          top = fmaxf(top, s);
+        }
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+        if (lane == 0) sh.xs[v3][dw] = top;
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.k_full);
+        if (it > 0 && !wait_warp(sh, &sh.v_empty, uint32_t(it - 1) & 1u, p.err)) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(smem + kV + tco(16 * dw + 2 * i + (lane >> 4), c)) = kx[i];
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.v_full);
+      }
+      ++it;
+      more = wk.next(p);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_inc<kRegsSoft>();
+    const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+    int it = 0, k0 = wk.k, u_dl = 0, u_rl = 0;
+    float M = -INFINITY, l = 0.0f, zs = 0.0f, cl = 0.0f;
+    float asc = 0.0f;  // factor of the sums in shared memory against O (0: nothing there yet)
+    int run = 0;       // tiles of this part of the unit so far
+    float4* acc = reinterpret_cast<float4*>(smem + kAcc) + 16 * half * 128 + row;  // [column / 4][row]
+    uint32_t mk[4] = {0u, 0u, 0u, 0u};  // drafted tokens this row sees
+    size_t orow = 0;
+    bool valid = false, some = false, more = true;
+    // Waits until the second product of tile j is complete.  A parity names a phase only
+    // among two: with a barrier for every other tile, and tile it - 2 waited for at tile it,
+    // the phase asked for is always the current one or the one before.
+    auto wait_pv = [&](int j) {
+      wait(sh, &sh.pv_done[j & 1], uint32_t(j >> 1) & 1u, p.err);
+      __syncwarp();
+    };
+    auto load_q = [&](const Walk& w) {
+      const int R = 128 * w.r + row, i = R / p.gqa;
+      valid = i < w.s.dl;
+      some = 128 * w.r + 32 * quarter < w.s.dl * p.gqa;  // any row of this warp
+      orow = (size_t(w.b) * p.T + i) * p.Hq + w.h * p.gqa + (R - i * p.gqa);
+      u_dl = w.s.dl;
+      u_rl = w.s.rl;
+      if (some) {
+        uint4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j] = valid ? __ldcg(reinterpret_cast<const uint4*>(p.q + orow * kHeadDim + 64 * half) + j)
+                       : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mk[j] = valid && j < p.W ? __ldcg(p.mask + (size_t(w.b) * p.T + i) * p.W + j) : 0u;
+          const int left = u_dl - 32 * j;
+          mk[j] &= left >= 32 ? kFull : left > 0 ? (1u << left) - 1u : 0u;
+        }
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2(x[e], T());
+            m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+        pair_sync(1 + quarter);
+        sh.xch[0][row][half] = m;
+        pair_sync(1 + quarter);
+        m = fmaxf(m, sh.xch[0][row][half ^ 1]);
+        pair_sync(1 + quarter);
+        // |q| < 2^e; e = 0 below 1
+        const int e = min(max(int((__float_as_uint(m) >> 23) & 0xff) - 126, 0), 126);
+        const float f = p.c_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
+        cl = 2.0f * fabsf(p.c_log2) * pow2i(e);
+        uint32_t qh[32];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 y = unpack2(x[c], T());
+            qh[4 * j + c] = pack_h2(y.x * f, y.y * f);
+          }
+        }
+        tc::st<32>(tc::lane_addr(tm + kColQ, warp, 32 * half), qh);
+        tc::wait_st();
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full);
+    };
+    load_q(wk);
+    while (more) {
+      const int buf = it & 1, v3 = it % 3;
+      const uint32_t tS = tm + uint32_t(buf) * kColS;
+      const bool raw = wk.raw();
+      // (after a wait that gave up every other one returns at once: the loop runs out by
+      // itself, and the pairs' barriers stay matched)
+      wait(sh, &sh.s_full[buf], uint32_t(it >> 1) & 1u, p.err);
+      if (it >= 2) wait_pv(it - 2);
+      __syncwarp();
+      tc::fence_after();
+      if (some) {
+        uint32_t sv[4][16], zr[2] = {0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc::ld<16>(tc::lane_addr(tS, warp, 64 * half + 16 * i), sv[i]);
+        if (!raw) tc::ld<2>(tc::lane_addr(tS, warp, 128 + 2 * half), zr);
+        tc::wait_ld();
+        float zb[2] = {__uint_as_float(zr[0]) * cl, __uint_as_float(zr[1]) * cl};
+        float mx = -INFINITY;
+        if (!raw) {
+          const int ng = (wk.s.np - wk.k * PPT) * (p.P / 32);  // groups of the tile that hold tokens (4 or more: all)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float a = __uint_as_float(sv[2 * i][0]);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) a = fmaxf(a, __uint_as_float(sv[2 * i + (j >> 4)][j & 15]));
+            if (2 * half + i < ng) {
+              mx = fmaxf(mx, fmaf(a, cl, zb[i]));
+            } else {
+              zb[i] = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sv[2 * i + (j >> 4)][j & 15] = 0u;
+            }
+          }
+        } else {
+          // bit j of vis[i]: the row sees token 32 i + j of its half
+          const int x0 = 128 * (wk.k - wk.s.ntp) + 64 * half;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int xw = x0 + 32 * i, in_window = u_rl - xw, d = xw - u_rl;  // first drafted token of the word
+            uint32_t vis = in_window >= 32 ? kFull : in_window > 0 ? (1u << in_window) - 1u : 0u;
+            if (d > -32) {
+              const int wd = d >> 5;
+              uint32_t a = 0u, b2 = 0u;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                a = j == wd ? mk[j] : a;
+                b2 = j == wd + 1 ? mk[j] : b2;
+              }
+              vis |= __funnelshift_r(a, b2, uint32_t(d) & 31u);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              uint32_t& s = sv[2 * i + (j >> 4)][j & 15];
+              s = ((vis >> j) & 1u) ? __float_as_uint(__uint_as_float(s) * cl) : 0xff800000u;
+              mx = fmaxf(mx, __uint_as_float(s));
+            }
+          }
+        }
+        sh.xch[buf][row][half] = mx;
+        pair_sync(1 + quarter);  // also: both threads of the row have read S
+        mx = fmaxf(mx, sh.xch[buf][row][half ^ 1]);
+        float sm;
+        if (!raw) {
+          sm = fmaxf(fmaxf(sh.smax[v3][0], sh.smax[v3][1]), fmaxf(sh.smax[v3][2], sh.smax[v3][3]));
+        } else {
+          sm = sh.xs[v3][0];
+#pragma unroll
+          for (int j = 1; j < kDeqWarps; ++j) sm = fmaxf(sm, sh.xs[v3][j]);
+        }
+        // sm < 2^lg; probabilities are carried as 2^(x - M + 7), so p * s starts below 2^7
+        const float lg = float(max(-20, int((__float_as_uint(sm) >> 23) & 0xff) - 126));
+        mx += lg;
+        float alpha = 1.0f;
+        if (mx > M + 8.0f) {  // p * s could pass 2^15
+          alpha = ex2(M - mx);  // M = -inf: 0
+          l *= alpha;
+          zs *= alpha;
+          asc *= alpha;
+          M = mx;
+        }
+        if (run > 0 && run % kFlush == 0) {
+          // O into the sums; it starts anew with this tile
+          wait_pv(it - 1);
+          tc::fence_after();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[16];
+            tc::ld<16>(tc::lane_addr(tm + kColO, warp, 64 * half + 16 * i), o);
+            tc::wait_ld();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float4& a = acc[(4 * i + j) * 128];
+              float4 x = asc != 0.0f ? a : make_float4(0.f, 0.f, 0.f, 0.f);
+              x.x = fmaf(x.x, asc, __uint_as_float(o[4 * j]) * alpha);
+              x.y = fmaf(x.y, asc, __uint_as_float(o[4 * j + 1]) * alpha);
+              x.z = fmaf(x.z, asc, __uint_as_float(o[4 * j + 2]) * alpha);
+              x.w = fmaf(x.w, asc, __uint_as_float(o[4 * j + 3]) * alpha);
+              a = x;
+            }
+          }
+          asc = 1.0f;
+        } else if (run > 0 && __any_sync(kFull, alpha != 1.0f)) {
+          wait_pv(it - 1);
+          tc::fence_after();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[16];
+            tc::ld<16>(tc::lane_addr(tm + kColO, warp, 64 * half + 16 * i), o);
+            tc::wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tc::st<16>(tc::lane_addr(tm + kColO, warp, 64 * half + 16 * i), o);
+          }
+        }
+        const float nm = M == -INFINITY ? 0.0f : 7.0f - M;
+        const float mul = raw ? 1.0f : cl;
+        float lp[4] = {0.0f, 0.0f, 0.0f, 0.0f}, zp[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 16 tokens: 8 columns of high parts, 8 of low parts
+          const float off = raw ? nm : zb[i >> 1] + nm;
+          uint32_t ph[8], pl[8];
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 s4 = *reinterpret_cast<const float4*>(&sh.vs[v3][64 * half + 16 * i + j]);
+            const float4 z4 = *reinterpret_cast<const float4*>(&sh.vz[v3][64 * half + 16 * i + j]);
+            float pr[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pr[e] = ex2(__fmaf_rn(__uint_as_float(sv[i][j + e]), mul, off));
+            lp[i] += (pr[0] + pr[1]) + (pr[2] + pr[3]);
+            zp[0] = fmaf(pr[0], z4.x, zp[0]);
+            zp[1] = fmaf(pr[1], z4.y, zp[1]);
+            zp[0] = fmaf(pr[2], z4.z, zp[0]);
+            zp[1] = fmaf(pr[3], z4.w, zp[1]);
+            pr[0] *= s4.x;
+            pr[1] *= s4.y;
+            pr[2] *= s4.z;
+            pr[3] *= s4.w;
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const uint32_t hp = pack_h2(pr[e], pr[e + 1]);
+              const float2 hf = __half22float2(u32_as_h2(hp));
+              ph[(j + e) / 2] = hp;
+              pl[(j + e) / 2] = pack_h2(pr[e] - hf.x, pr[e + 1] - hf.y);
+            }
+          }
+          tc::st<8>(tc::lane_addr(tS, warp, 32 * half + 8 * i), ph);
+          tc::st<8>(tc::lane_addr(tS, warp, 64 + 32 * half + 8 * i), pl);
+        }
+        l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
+        zs += zp[0] + zp[1];
+        tc::wait_st();
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_full[buf]);
+
+      const bool last = wk.last, from0 = k0 == 0, to_end = wk.k == wk.s.nt - 1;
+      more = wk.next(p);
+      if (last) {
+        // what this unit's rows need, before the next unit's query replaces it
+        const bool v0 = valid, some0 = some;
+        const size_t out_row = orow;
+        const float M0 = M;
+        float l0 = l, z0 = zs;
+        if (more) load_q(wk);
+        wait_pv(it);
+        tc::fence_after();
+        if (some0) {
+          pair_sync(1 + quarter);
+          sh.xch[0][row][half] = l0;
+          sh.xch[1][row][half] = z0;
+          pair_sync(1 + quarter);
+          l0 += sh.xch[0][row][half ^ 1];
+          z0 += sh.xch[1][row][half ^ 1];
+          pair_sync(1 + quarter);
+          const bool whole = from0 && to_end;
+          const float inv = whole ? (l0 > 0.0f ? 1.0f / l0 : 0.0f) : 1.0f;
+          float* dst = whole ? p.out + out_row * kHeadDim
+                             : p.part + (size_t(2 * cta + (from0 ? 1 : 0)) * 128 + row) * kPart;
+          bool bad = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[16];
+            tc::ld<16>(tc::lane_addr(tm + kColO, warp, 64 * half + 16 * i), o);
+            tc::wait_ld();
+            if (v0) {
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) {
+                if (asc != 0.0f) {
+                  const float4 a = acc[(4 * i + j / 4) * 128];
+                  o[j] = __float_as_uint(fmaf(a.x, asc, __uint_as_float(o[j])));
+                  o[j + 1] = __float_as_uint(fmaf(a.y, asc, __uint_as_float(o[j + 1])));
+                  o[j + 2] = __float_as_uint(fmaf(a.z, asc, __uint_as_float(o[j + 2])));
+                  o[j + 3] = __float_as_uint(fmaf(a.w, asc, __uint_as_float(o[j + 3])));
+                }
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  x[e] = fmaf(2.0f, __uint_as_float(o[j + e]), z0) * inv;
+                  bad |= !(fabsf(x[e]) < INFINITY);
+                }
+                *reinterpret_cast<float4*>(dst + 64 * half + 16 * i + j) = make_float4(x[0], x[1], x[2], x[3]);
+              }
+            }
+          }
+          if (v0) {
+            if (bad || !(l0 < INFINITY)) flag_error(p.err, KVQ_DEV_ERR_RANGE);
+            if (!whole && half == 0) {
+              dst[128] = M0;
+              dst[129] = l0;
+            }
+          }
+        }
+        M = -INFINITY;
+        l = zs = asc = 0.0f;
+        run = -1;
+        k0 = more ? wk.k : 0;
+      }
+      ++it;
+      ++run;
+    }
+  }
+  // ---------------------------------------------------------------- leave
+  pdl_trigger();
+  tc::fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == kIssuer) tc::dealloc(tm, 512);
+}
+
+// Joins the parts of the units that range boundary blockIdx.x + 1 cuts, 16 rows a block.
+template <typename T>
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ TreeParams p) {
+  __shared__ Line line;
+  pdl_wait();
+  pdl_trigger();
+  const int cta = blockIdx.x + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  line_find<256>(p, line, cta, p.n_ctas, false);
+  const int W = line.W, n = line.n;
+  if (cta >= n) return;
+  Walk wk;
+  const int at = range_at(cta, W, n);
+  wk.start(p, line.b0, line.base0, at, at + 1);
+  if (wk.k == 0) return;  // the boundary falls between units
+  const int u0 = at - wk.k, c0 = range_owner(u0, W, n), c1 = range_owner(u0 + wk.s.nt - 1, W, n);
+  if (cta != c0 + 1) return;  // the unit's first boundary joins it
+  for (int r = 16 * blockIdx.y + warp; r < 16 * blockIdx.y + 16; r += 8) {
+    const int R = 128 * wk.r + r, i = R / p.gqa;
+    if (i >= wk.s.dl) return;
+    float M = -INFINITY;
+    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part + (size_t(2 * c + (c == c0)) * 128 + r) * kPart + 128));
+    float l = 0.0f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const float* part = p.part + (size_t(2 * c + (c == c0)) * 128 + r) * kPart;
+      const float f = M == -INFINITY ? 0.0f : ex2(__ldcg(part + 128) - M);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(part) + lane);
+      l = fmaf(f, __ldcg(part + 129), l);
+      o.x = fmaf(f, x.x, o.x);
+      o.y = fmaf(f, x.y, o.y);
+      o.z = fmaf(f, x.z, o.z);
+      o.w = fmaf(f, x.w, o.w);
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const size_t row = (size_t(wk.b) * p.T + i) * p.Hq + wk.h * p.gqa + (R - i * p.gqa);
+    reinterpret_cast<float4*>(p.out + row * kHeadDim)[lane] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  }
+}
+
+template <typename T, int KB>
+cudaError_t launch_t(const TreeParams& p, cudaStream_t stream) {
+  static int seen[64];
+  const int bytes = int(kRec + kRecStages * uint32_t(128 / p.P) * p.L.record);
+  cudaError_t e = ensure_dynamic_smem(tree_kernel<T, KB>, bytes, seen);
+  if (e != cudaSuccess) return e;
+  // the register split waits for good on a build that launches with fewer registers
+  static int regs;
+  int r = __atomic_load_n(&regs, __ATOMIC_ACQUIRE);
+  if (r == 0) {
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, tree_kernel<T, KB>);
+    if (e != cudaSuccess) return e;
+    r = a.numRegs;
+    __atomic_store_n(&regs, r, __ATOMIC_RELEASE);
+  }
+  if (r < kRegsLaunch) return cudaErrorInvalidConfiguration;
+  e = launch_pdl(tree_kernel<T, KB>, dim3(p.n_ctas), dim3(kThreads), size_t(bytes), stream, p);
+  if (e != cudaSuccess || p.n_ctas < 2) return e;
+  return launch_pdl(merge_kernel<T>, dim3(p.n_ctas - 1, 8), dim3(256), 0, stream, p);
+}
+
+template <typename T>
+cudaError_t launch(const TreeParams& p, cudaStream_t stream) {
+  switch (p.k / 16) {
+    case 0: return launch_t<T, 0>(p, stream);
+    case 1: return launch_t<T, 1>(p, stream);
+    case 2: return launch_t<T, 2>(p, stream);
+    case 4: return launch_t<T, 4>(p, stream);
+    case 8: return launch_t<T, 8>(p, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace tree
+}  // namespace kvq
