@@ -14,8 +14,10 @@
 //
 // Per tile, with thread roles that run ahead of one another through mbarriers:
 //   producer   1 warp    copies the page records (one bulk copy each, three tiles ahead);
-//   dequant    8 warps   writes the keys and the value codes as fp16 operands;
-//   issuer     1 thread  S = Q K^T, then O += P V of the tile before (tcgen05, M = 128);
+//   mover      1 warp    lists where the boosted channels' plane-B codes go;
+//   dequant    8 warps   write the keys of a tile, then the value codes of the tile before,
+//                        as fp16 operands;
+//   issuer     1 warp    S = Q K^T, then O += P V of the tile before (tcgen05, M = 128);
 //   softmax    8 warps   a thread per (row, half of the tile's tokens): S from tensor
 //                        memory, running maximum, P back over S.
 // Two S / P buffers of 144 columns, O (128 columns) and Q (64 columns) fill tensor memory.
@@ -29,7 +31,8 @@
 //    in columns 128..131 of S;
 //  * the query enters as q * 2^-e (exact), e from its largest element;
 //  * the value scale is folded into the probability, P = p * sV as a high and a low fp16
-//    part, so the value operand is the 2-bit codes themselves; sum p z is added in fp32.
+//    part, so the value operand is the 2-bit codes themselves, centred (code - 1.5) so that
+//    sums do not cancel against the zero points; sum p (z + 1.5 sV) is added in fp32.
 //    The running reference M covers the largest p * sV of a tile, so P stays inside fp16
 //    whatever the value scales are;
 //  * window and drafted tokens go through the same products: K / 2 and V * 2^-e_t in fp16,
@@ -43,12 +46,15 @@
 namespace kvq {
 namespace tree {
 
+// The code of all roles together has to stay in the instruction caches, so the roles' loops
+// are rolled (unrolled, 130 KB of code, the same work took XX us instead of YY).
 constexpr int kSoftWarps = 8, kDeqWarps = 8;
-constexpr int kIssuer = kSoftWarps + kDeqWarps, kProducer = kIssuer + 1;
-constexpr int kThreads = 640;  // 5 warpgroups: two of softmax, two of dequant, one with the issuer and the producer
-// Registers a thread: at launch, then by role (setmaxnreg): 2 x 128 + 2 x 80 + 64 = 5 x 96,
-// so the split draws on exactly what the block was launched with.
-constexpr int kRegsLaunch = 96, kRegsSoft = 128, kRegsDeq = 80, kRegsRest = 64;
+constexpr int kIssuer = kSoftWarps + kDeqWarps, kProducer = kIssuer + 1, kMover = kIssuer + 2;
+constexpr int kThreads = 640;  // 5 warpgroups: two of softmax, two of dequant, one of single warps
+// Registers a thread: at launch, then by role (setmaxnreg): 2 x 120 + 2 x 88 + 64 = 5 x 96,
+// so the split draws on exactly what the block was launched with.  The shared memory leaves
+// next to no L1, so a register spilled in a role's loop costs an L2 access.
+constexpr int kRegsLaunch = 96, kRegsSoft = 120, kRegsDeq = 88, kRegsRest = 64;
 static_assert(2 * kRegsSoft + 2 * kRegsDeq + kRegsRest <= 5 * kRegsLaunch, "register split");
 constexpr int kRecStages = 3;
 // The tensor cores round their fp32 accumulator toward zero: 16 products a tile shrink a long
@@ -74,6 +80,12 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t x;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(x));
   return x != 0;
+}
+// Waits for this thread's tensor-memory loads; naming the registers keeps their uses behind it.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
@@ -126,7 +138,7 @@ struct Walk {
   Seq s;
   int b, h, r, k;  // sequence, kv head, row tile, tile of the unit
   int pos, end;
-  bool first, last;  // of this CTA's part of the unit
+  bool first;        // of this CTA's part of the unit
   __device__ __forceinline__ void start(const TreeParams& p, int b0, int base, int from, int to) {
     b = b0;
     seq_load(p, b, s);
@@ -137,27 +149,23 @@ struct Walk {
     pos = from;
     end = to;
     first = true;
-    last = k == s.nt - 1 || pos == end - 1;
   }
   __device__ __forceinline__ bool next(const TreeParams& p) {
     if (++pos >= end) return false;
-    first = false;
-    if (++k == s.nt) {
-      k = 0;
-      first = true;
-      if (++r == s.nrt) {
-        r = 0;
-        if (++h == p.Hkv) {
-          h = 0;
-          do {
-            ++b;
-            seq_load(p, b, s);
-          } while (s.nrt == 0 && b < p.batch - 1);
-        }
-      }
-    }
-    last = k == s.nt - 1 || pos == end - 1;
+    first = ++k == s.nt;
+    if (first) next_unit(p);
     return true;
+  }
+  __device__ __forceinline__ void next_unit(const TreeParams& p) {
+    k = 0;
+    if (++r < s.nrt) return;
+    r = 0;
+    if (++h < p.Hkv) return;
+    h = 0;
+    do {
+      ++b;
+      seq_load(p, b, s);
+    } while (s.nrt == 0 && b < p.batch - 1);
   }
   __device__ __forceinline__ bool raw() const { return k >= s.ntp; }
 };
@@ -176,6 +184,7 @@ template <int NT>
 __device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta, int ctas, bool flag) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int total = 0;
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     int run = 0, at = 0;
     if (pass == 1) {
@@ -186,6 +195,7 @@ __device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta
       if (cta >= min(ctas, total)) break;
       at = range_at(cta, total, min(ctas, total));
     }
+#pragma unroll 1
     for (int base = 0; base < p.batch; base += NT) {
       const int b = base + tid;
       int x = 0;
@@ -203,6 +213,7 @@ __device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta
       if (lane == 31) ln.sums[warp] = incl;
       __syncthreads();
       int before = run, all = 0;
+#pragma unroll 4
       for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) before += ln.sums[w];
         all += ln.sums[w];
@@ -219,31 +230,50 @@ __device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta
   __syncthreads();
 }
 
+// Moves of one page's boosted codes, by the words that receive them (8 lists, see
+// list_moves): {rotation | source word << 8, mask}, padded to an even length.
+struct Moves {
+  uint2 m[8][18];
+  int n[8];
+};
+
+// MOVES: whether the kernel lists moves (some but not all channels boosted).
+template <bool MOVES>
 struct Shared {
-  uint64_t rec_full[kRecStages], rec_empty[kRecStages], k_full, k_empty, v_full, v_empty, s_full[2], p_full[2], pv_done[2],
-      q_full;
+  uint64_t rec_full[kRecStages], rec_empty[kRecStages], mv_full[kRecStages], k_full, k_empty, v_full, v_empty, s_full[2],
+      p_full[2], pv_done[2], q_full;
   uint32_t tmem;
   int abort;
   float xch[2][128][2];                 // [parity][row][half]
   __align__(16) float vs[3][128];       // value scale (raw tiles: 2^e_t / 2) of a tile's tokens
-  __align__(16) float vz[3][128];       // value zero point
+  __align__(16) float vz[3][128];       // value zero point + 1.5 scales
   float smax[3][4];                     // largest value scale of a page tile's groups
   float xs[3][kDeqWarps];               // the same of a raw tile, by the warp that wrote it
-  __align__(16) uint2 tab[kDeqWarps][4][34];  // moves of boosted codes: {rotation | source word << 8, mask} per word
   Line line;
+  __align__(16) Moves moves[MOVES ? kRecStages : 1][MOVES ? 4 : 1];  // [stage][page of the tile]
 };
 
-// Waits for a phase; false once any wait of the CTA has given up.
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, int32_t* err) {
-  if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
-  if (mbar_wait_bounded(bar, parity)) return true;
-  flag_error(err, KVQ_DEV_ERR_TIMEOUT);
-  *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-  return false;
+// Waits for a phase (about a second at most); false once any wait of the CTA has given up.
+template <typename S>
+__device__ __forceinline__ bool wait(S& sh, uint64_t* bar, uint32_t parity, int32_t* err) {
+  bool ok = mbar_try_wait_suspend(bar, parity, 20000u);
+  if (!ok) {
+    const uint32_t t0 = uint32_t(clock());
+    volatile int* abort = &sh.abort;
+    do {
+      if (*abort) return false;
+      ok = mbar_try_wait_suspend(bar, parity, 20000u);
+    } while (!ok && uint32_t(clock()) - t0 < (1u << 31));
+    if (!ok) {
+      flag_error(err, KVQ_DEV_ERR_TIMEOUT);
+      *abort = 1;
+    }
+  }
+  return ok;
 }
-
 // The same by a whole warp, with one answer for all lanes.
-__device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t parity, int32_t* err) {
+template <typename S>
+__device__ __forceinline__ bool wait_warp(S& sh, uint64_t* bar, uint32_t parity, int32_t* err) {
   return __all_sync(kFull, wait(sh, bar, parity, err));
 }
 
@@ -251,132 +281,138 @@ constexpr int kPart = 132;  // floats of a partial row: unnormalised output, ref
 
 // ---------------------------------------------------------------- dequantization
 
-// The boosted channels of a page whose plane-A code sits in an odd (half = 1) or even word:
-// for each of the four words q (word 2q + half), the rotation that brings the plane-B code
-// of row j to its channel's bits.  Lists are padded to an even length; counts in n[4].
+// A dequant warp takes one pass a (0, 1) of the plane-A words 2q + half (q = 0..3) of a
+// token: channels 16 s + 8 r + 2 q + f with s = 4 half + 2 a + (0, 1).  The plane-B codes of
+// its boosted channels are gathered into two words, for q = 2 qp and 2 qp + 1: code of byte
+// i = 2 (s & 1) + r, f at bit 8 i + 4 f + 2 (q & 1).  List 4 half + 2 a + qp of a page's
+// moves holds, for each of its boosted channels there, the rotation that brings the plane-B
+// code to that bit.  One warp lists a page's moves; the indices are those of the record.
 template <int KB>
-__device__ __forceinline__ void boost_moves(const uint8_t* idx, int half, uint2 (*tab)[34], int (&n)[4], int lane) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) n[q] = 0;
-#pragma unroll
+__device__ __forceinline__ void list_moves(const uint8_t* idx, Moves& mv, int lane) {
+  int count = 0;  // of list `lane`
+#pragma unroll 1
   for (int j0 = 0; j0 < 16 * KB; j0 += 32) {
     const int j = j0 + lane;
-    int dq = -1;
+    int list = 8 + (lane & 7);  // none
     uint2 m = make_uint2(0u, 0u);
     if (j < 16 * KB) {
-      const int src = boost_pos(j, KB), dst = key_pos(idx[j] & 127);
-      if (((dst >> 4) & 1) == half) dq = dst >> 5;
-      const int sb = elem_bit(src & 15), db = elem_bit(dst & 15);
-      m = make_uint2(uint32_t((sb - db) & 31) | (uint32_t(src >> 4) << 8), 3u << db);
+      const int c = idx[j] & 127, s = c >> 4, r = (c >> 3) & 1, q = (c >> 1) & 3, f = c & 1;
+      const int src = boost_pos(j, KB), db = 8 * (2 * (s & 1) + r) + 4 * f + 2 * (q & 1);
+      list = 4 * (s >> 2) + 2 * ((s >> 1) & 1) + (q >> 1);
+      m = make_uint2(uint32_t((elem_bit(src & 15) - db) & 31) | (uint32_t(src >> 4) << 8), 3u << db);
     }
+    const uint32_t same = __match_any_sync(kFull, list);
+    const int at = __shfl_sync(kFull, count, list & 7) + __popc(same & ((1u << lane) - 1u));
+    // 16 channels a list; more only where a record repeats an index (unused rows, code zero)
+    if (list < 8 && at < 16) mv.m[list][at] = m;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t bal = __ballot_sync(kFull, dq == q);
-      if (dq == q) tab[q][min(n[q] + __popc(bal & ((1u << lane) - 1u)), 32)] = m;
-      n[q] += __popc(bal);
+    for (int l = 0; l < 8; ++l) {
+      const int n = __popc(__ballot_sync(kFull, list == l));
+      if (lane == l) count = min(count + n, 16);
     }
   }
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    n[q] = min(n[q], 32);  // 16 channels a word; more only in a record that repeats an index
-    if (lane == 0 && (n[q] & 1)) tab[q][n[q]] = make_uint2(0u, 0u);
+  __syncwarp();
+  if (lane < 8) {
+    if (count & 1) mv.m[lane][count] = make_uint2(0u, 0u);
+    mv.n[lane] = count;
   }
   __syncwarp();
 }
 
-// Keys of token `row` of the tile (token tp of the page record), the 64 channels of `half`.
+// Keys of token `row` of the tile (token tp of the page record): the 32 channels of (half, a).
 template <typename T, int KB>
-__device__ __forceinline__ void key_row(const TreeParams& p, const uint8_t* rec, int tp, int row, int half, uint8_t* smem,
-                                        const uint2 (*tab)[34], const int (&n)[4]) {
+__device__ __forceinline__ void key_row(const TreeParams& p, const uint8_t* rec, int tp, int row, int half, int a,
+                                        uint8_t* smem, const Moves& mv) {
   const uint4 w0 = lds128(rec + p.L.k_codes + tp * 32), w1 = lds128(rec + p.L.k_codes + tp * 32 + 16);
   const uint32_t w[4] = {half ? w0.y : w0.x, half ? w0.w : w0.z, half ? w1.y : w1.x, half ? w1.w : w1.z};
-  uint32_t wb[4] = {0u, 0u, 0u, 0u};
+  uint32_t wb[4];
   if constexpr (KB == 8) {  // every channel boosted: plane B has the layout of plane A
     const uint4 b0 = lds128(rec + p.L.kb_codes + tp * 32), b1 = lds128(rec + p.L.kb_codes + tp * 32 + 16);
-    wb[0] = half ? b0.y : b0.x;
-    wb[1] = half ? b0.w : b0.z;
-    wb[2] = half ? b1.y : b1.x;
-    wb[3] = half ? b1.w : b1.z;
+    wb[0] = (half ? b0.y : b0.x) >> (2 * a);
+    wb[1] = (half ? b0.w : b0.z) >> (2 * a);
+    wb[2] = (half ? b1.y : b1.x) >> (2 * a);
+    wb[3] = (half ? b1.w : b1.z) >> (2 * a);
   } else if constexpr (KB > 0) {
     const uint8_t* brow = rec + p.L.kb_codes + tp * (4 * KB);
     uint32_t src0 = 0u, src1 = 0u;
-    if constexpr (KB <= 2) {
-      src0 = lds32(brow);
-      if constexpr (KB == 2) src1 = lds32(brow + 4);
+    if constexpr (KB == 1) src0 = lds32(brow);
+    if constexpr (KB == 2) {
+      const uint2 x = lds64(brow);
+      src0 = x.x;
+      src1 = x.y;
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int qp = 0; qp < 2; ++qp) {
+      const int list = 4 * half + 2 * a + qp, n = mv.n[list];
       uint32_t acc = 0u;
-      for (int e = 0; e < n[q]; e += 2) {
-        const uint4 m = *reinterpret_cast<const uint4*>(&tab[q][e]);
-        uint32_t a, b;
+#pragma unroll 2
+      for (int e = 0; e < n; e += 2) {
+        const uint4 m = *reinterpret_cast<const uint4*>(&mv.m[list][e]);
+        uint32_t x, y;
         if constexpr (KB == 1) {
-          a = b = src0;
+          x = y = src0;
         } else if constexpr (KB == 2) {
-          a = (m.x >> 8) ? src1 : src0;
-          b = (m.z >> 8) ? src1 : src0;
+          x = (m.x >> 8) ? src1 : src0;
+          y = (m.z >> 8) ? src1 : src0;
         } else {
-          a = lds32(brow + 4 * (m.x >> 8));
-          b = lds32(brow + 4 * (m.z >> 8));
+          x = lds32(brow + 4 * (m.x >> 8));
+          y = lds32(brow + 4 * (m.z >> 8));
         }
-        acc |= (__funnelshift_r(a, a, m.x) & m.y) | (__funnelshift_r(b, b, m.z) & m.w);
+        acc |= (__funnelshift_r(x, x, m.x) & m.y) | (__funnelshift_r(y, y, m.z) & m.w);
       }
-      wb[q] = acc;
+      wb[2 * qp] = acc;
+      wb[2 * qp + 1] = acc >> 2;
     }
   }
-  const int gp = tp >> 5;
+  uint32_t hi[4][4], lo[4][4];  // [q][i]
+  const uint8_t* sc = rec + p.L.k_scale + (tp >> 5) * 256 + 64 * (2 * half + a);
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    uint32_t hi[4][4], lo[4][4];  // [word q][k-step bit, 8-channel bit]
-    const uint8_t* sc = rec + p.L.k_scale + gp * 256 + 64 * (2 * half + a);
+  for (int q = 0; q < 4; ++q) {
+    uint32_t u[4];
+    e2m1_pairs(code_pass(w[q], a), u[0], u[1], u[2], u[3]);
+    if constexpr (KB > 0) {
+      uint32_t ub[4];
+      e2m1_pairs(wb[q] & 0x33333333u, ub[0], ub[1], ub[2], ub[3]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t u[4];
-      e2m1_pairs(code_pass(w[q], a), u[0], u[1], u[2], u[3]);
-      if constexpr (KB > 0) {
-        uint32_t ub[4];
-        e2m1_pairs(code_pass(wb[q], a), ub[0], ub[1], ub[2], ub[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          u[i] = h2_as_u32(__hfma2(u32_as_h2(ub[i]), __float2half2_rn(0.25f), u32_as_h2(u[i])));
-      }
-      const uint4 s4 = lds128(sc + 16 * q);
-      const uint32_t s[4] = {meta_h2(s4.x, T()), meta_h2(s4.y, T()), meta_h2(s4.z, T()), meta_h2(s4.w, T())};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 x = __hmul2(u32_as_h2(u[i]), u32_as_h2(s[i]));
-        hi[q][i] = h2_as_u32(x);
-        lo[q][i] = h2_as_u32(__hfma2(u32_as_h2(u[i]), u32_as_h2(s[i]), __hneg2(x)));
-      }
+      for (int i = 0; i < 4; ++i)
+        u[i] = h2_as_u32(__hfma2(u32_as_h2(ub[i]), __float2half2_rn(0.25f), u32_as_h2(u[i])));
     }
+    const uint4 s4 = lds128(sc + 16 * q);
+    const uint32_t s[4] = {meta_h2(s4.x, T()), meta_h2(s4.y, T()), meta_h2(s4.z, T()), meta_h2(s4.w, T())};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t at = tco(row, 8 * half + 4 * a + i);
-      *reinterpret_cast<uint4*>(smem + kKhi + at) = make_uint4(hi[0][i], hi[1][i], hi[2][i], hi[3][i]);
-      *reinterpret_cast<uint4*>(smem + kKlo + at) = make_uint4(lo[0][i], lo[1][i], lo[2][i], lo[3][i]);
+      const __half2 x = __hmul2(u32_as_h2(u[i]), u32_as_h2(s[i]));
+      hi[q][i] = h2_as_u32(x);
+      lo[q][i] = h2_as_u32(__hfma2(u32_as_h2(u[i]), u32_as_h2(s[i]), __hneg2(x)));
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t at = tco(row, 8 * half + 4 * a + i);
+    *reinterpret_cast<uint4*>(smem + kKhi + at) = make_uint4(hi[0][i], hi[1][i], hi[2][i], hi[3][i]);
+    *reinterpret_cast<uint4*>(smem + kKlo + at) = make_uint4(lo[0][i], lo[1][i], lo[2][i], lo[3][i]);
   }
 }
 
-// Value codes of group g of the tile (group gp of the page record): channels of m-tiles
-// 4 mh .. 4 mh + 3, tokens contiguous (K-major operand of the second product).
-__device__ __forceinline__ void value_codes(const TreeParams& p, const uint8_t* rec, int gp, int g, int mh, uint8_t* smem,
-                                            int lane) {
+// Value codes of group g of the tile (group gp of the page record), pass a: channels of
+// m-tiles 4 mh .. 4 mh + 3, tokens contiguous (K-major operand of the second product), as
+// (code - 1.5) / 2.
+__device__ __forceinline__ void value_codes(const TreeParams& p, const uint8_t* rec, int gp, int g, int mh, int a,
+                                            uint8_t* smem, int lane) {
   const int w = lane & 7, m3 = lane >> 3, m = 4 * mh + m3;
   const uint8_t* vq = rec + p.L.v_codes + (((2 * gp + mh) * 32 + 4 * w) * 4 + m3) * 4;
-  uint32_t x[4];
+  const __half2 mid = __float2half2_rn(-0.75f);
+  uint32_t u[4][4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) x[q] = lds32(vq + 16 * q);
+  for (int q = 0; q < 4; ++q) {
+    e2m1_pairs(code_pass(lds32(vq + 16 * q), a), u[q][0], u[q][1], u[q][2], u[q][3]);
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    uint32_t u[4][4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) e2m1_pairs(code_pass(x[q], a), u[q][0], u[q][1], u[q][2], u[q][3]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)  // byte 2u + v: tokens 8u.., channels 8v..
-      *reinterpret_cast<uint4*>(smem + kV + (2 * m + (i & 1)) * 2048 + (4 * g + 2 * a + (i >> 1)) * 128 + w * 16) =
-          make_uint4(u[0][i], u[1][i], u[2][i], u[3][i]);
+    for (int i = 0; i < 4; ++i) u[q][i] = h2_as_u32(__hadd2(u32_as_h2(u[q][i]), mid));
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // byte 2u + v: tokens 8u.., channels 8v..
+    *reinterpret_cast<uint4*>(smem + kV + (2 * m + (i & 1)) * 2048 + (4 * g + 2 * a + (i >> 1)) * 128 + w * 16) =
+        make_uint4(u[0][i], u[1][i], u[2][i], u[3][i]);
 }
 
 // Window and drafted tokens: source row of token x of the raw sequence.
@@ -399,20 +435,98 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x, uint32_t expo, bool& bad
   return (a ? 0u : x & 0xffffu) | (b ? 0u : x & 0xffff0000u);
 }
 
+// ---------------------------------------------------------------- softmax
+
+// The 64 logits of one row at tensor-memory columns tR .. tR + 63 into probabilities
+// 2^(cl S + off) (off0 for the first 32 tokens, off1 for the others; 0 where the token's bit
+// of see0 / see1 is clear), times the tokens' value scales, as fp16 high and low parts in the
+// same columns: 16 tokens in 8 + 8.  Adds their sum to l and their sum with vz to zs.
+// MASK: whether the bits differ within a word.
+template <bool MASK>
+__device__ __forceinline__ void weights(uint32_t tR, float cl, float off0, float off1, uint32_t see0, uint32_t see1,
+                                        const float* vs, const float* vz, float& l, float& zs) {
+  float lp[4] = {0.0f, 0.0f, 0.0f, 0.0f}, zp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    uint32_t sx[16];
+    tc::ld<16>(tR + 16 * i, sx);
+    const float off = i < 2 ? off0 : off1;
+    const uint32_t see = (i < 2 ? see0 : see1) >> (16 * (i & 1));
+    wait_ld(sx);
+    uint32_t ph[8], pl[8];
+    float pr[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      pr[j] = ex2(__fmaf_rn(__uint_as_float(sx[j]), cl, off));
+      if (MASK) pr[j] = ((see >> j) & 1u) ? pr[j] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      const float4 s4 = *reinterpret_cast<const float4*>(vs + 16 * i + j);
+      const float4 z4 = *reinterpret_cast<const float4*>(vz + 16 * i + j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) lp[e] += pr[j + e];
+      zp[0] = fmaf(pr[j], z4.x, zp[0]);
+      zp[1] = fmaf(pr[j + 1], z4.y, zp[1]);
+      zp[2] = fmaf(pr[j + 2], z4.z, zp[2]);
+      zp[3] = fmaf(pr[j + 3], z4.w, zp[3]);
+      pr[j] *= s4.x;
+      pr[j + 1] *= s4.y;
+      pr[j + 2] *= s4.z;
+      pr[j + 3] *= s4.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      ph[j] = pack_h2(pr[2 * j], pr[2 * j + 1]);
+      const float2 hf = __half22float2(u32_as_h2(ph[j]));
+      pl[j] = pack_h2(pr[2 * j] - hf.x, pr[2 * j + 1] - hf.y);
+    }
+    tc::st<8>(tR + 16 * i, ph);
+    tc::st<8>(tR + 16 * i + 8, pl);
+  }
+  l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
+  zs += (zp[0] + zp[1]) + (zp[2] + zp[3]);
+}
+
+// The largest of the 32 values at tensor-memory columns tR .. tR + 31 whose bit of see is set
+// (MASK), -inf if there is none; masked values may be no number.
+template <bool MASK>
+__device__ __forceinline__ float largest(uint32_t tR, uint32_t see) {
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    uint32_t x[16];
+    tc::ld<16>(tR + 16 * i, x);
+    wait_ld(x);
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      a = fmaxf(a, !MASK || ((see >> j) & 1u) ? __uint_as_float(x[j]) : -INFINITY);
+      b = fmaxf(b, !MASK || ((see >> (j + 1)) & 1u) ? __uint_as_float(x[j + 1]) : -INFINITY);
+    }
+    m = fmaxf(m, fmaxf(a, b));
+    see >>= 16;
+  }
+  return m;
+}
+
 // ---------------------------------------------------------------- the kernel
 
 template <typename T, int KB>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Shared sh;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr bool kMoves = KB > 0 && KB < 8;
+  __shared__ Shared<kMoves> sh;
+  // (taken from lane 0, so that the compiler knows the roles' branches to be uniform)
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
 
   if (warp == kIssuer) tc::alloc(&sh.tmem, 512);
   if (tid == 0) {
     for (int i = 0; i < kRecStages; ++i) {
       mbar_init(&sh.rec_full[i], 1);
       mbar_init(&sh.rec_empty[i], kDeqWarps);
+      mbar_init(&sh.mv_full[i], 1);
     }
     mbar_init(&sh.k_full, kDeqWarps);
     mbar_init(&sh.k_empty, 1);
@@ -435,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tm = sh.tmem;
+  const uint32_t tm = __shfl_sync(kFull, sh.tmem, 0);
   const int W = sh.line.W, n_ctas = sh.line.n, cta = blockIdx.x;
   const bool idle = cta >= n_ctas;
   Walk wk;
@@ -496,14 +610,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       if (!ok) return;
       tc::fence_after();
       if (elect_one()) {
-        if (praw) {
-#pragma unroll
-          for (int s = 0; s < 16; ++s)
-            tc::mma(tm + kColO, tP + 8 * s, tc::smem_desc(sV + (s & 7) * 4096, 2048, 128), kIdMn, s > 0 || !pfresh);
-        } else {
-#pragma unroll
-          for (int s = 0; s < 16; ++s)
-            tc::mma(tm + kColO, tP + 8 * s, tc::smem_desc(sV + (s & 7) * 256, 128, 2048), kIdLo, s > 0 || !pfresh);
+        // 16 tokens a step: the raw tile's rows are tokens (MN-major), the codes' are channels
+        const uint64_t b0 = praw ? tc::smem_desc(sV, 2048, 128) : tc::smem_desc(sV, 128, 2048);
+        const uint32_t step = praw ? 4096 / 16 : 256 / 16, id = praw ? kIdMn : kIdLo;
+#pragma unroll 1
+        for (uint32_t s = 0; s < 8; ++s) {
+          tc::mma(tm + kColO, tP + 16 * s, b0 + s * step, id, s > 0 || !pfresh);
+          tc::mma(tm + kColO, tP + 16 * s + 8, b0 + s * step, id, 1u);
         }
         tc::commit(&sh.v_empty);
         tc::commit(&sh.pv_done[j & 1]);
@@ -512,7 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     };
     int run = 0;  // tiles of this CTA's part of the unit so far
     while (more && ok) {
-      if (wk.first) {
+      const bool first = __any_sync(kFull, wk.first), raw = __any_sync(kFull, wk.raw());  // the same in all lanes
+      if (first) {
         if (it > 0) second(it - 1);
         ok = ok && wait_warp(sh, &sh.q_full, uint32_t(seg++) & 1u, p.err);
         run = 0;
@@ -522,58 +636,92 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       tc::fence_after();
       const uint32_t dS = tm + uint32_t(it & 1) * kColS;
       if (elect_one()) {
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-          tc::mma(dS, tm + kColQ + 8 * s, tc::smem_desc(sKh + s * 256, 128, 2048), kIdHi, s > 0);
-        if (!wk.raw()) {
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-            tc::mma(dS, tm + kColQ + 8 * s, tc::smem_desc(sKl + s * 256, 128, 2048), kIdLo, 1u);
+        const uint64_t bh = tc::smem_desc(sKh, 128, 2048), bl = tc::smem_desc(sKl, 128, 2048);
+#pragma unroll 1
+        for (uint32_t s = 0; s < 8; ++s) tc::mma(dS, tm + kColQ + 8 * s, bh + s * (256 / 16), kIdHi, s > 0);
+        if (!raw) {
+#pragma unroll 1
+          for (uint32_t s = 0; s < 8; ++s) tc::mma(dS, tm + kColQ + 8 * s, bl + s * (256 / 16), kIdLo, 1u);
         }
         tc::commit(&sh.k_empty);
         tc::commit(&sh.s_full[it & 1]);
       }
       __syncwarp();
-      if (!wk.first) second(it - 1);
-      praw = wk.raw();
+      if (!first) second(it - 1);
+      praw = raw;
       pfresh = run++ % kFlush == 0;
       ++it;
-      more = wk.next(p);
+      more = __any_sync(kFull, wk.next(p));
     }
     if (ok) second(it - 1);
     // the products have completed before the operands' memory is released
     if (ok) wait_warp(sh, &sh.pv_done[(it - 1) & 1], uint32_t((it - 1) >> 1) & 1u, p.err);
+    } else if (kMoves && warp == kMover) {
+      // ---------------------------------------------------------- moves of boosted codes
+      if constexpr (kMoves) {
+        int n = 0;
+        bool more = true;
+        while (more) {
+          if (!wk.raw()) {
+            const int st = n % kRecStages, npg = min(PPT, wk.s.np - wk.k * PPT);
+            // (a stage that is full again has been read out, its moves too)
+            if (!wait_warp(sh, &sh.rec_full[st], uint32_t(n / kRecStages) & 1u, p.err)) break;
+            for (int i = 0; i < npg; ++i)
+              list_moves<KB>(smem + kRec + st * stage_bytes + i * p.L.record + p.L.boost_idx, sh.moves[st][i], lane);
+            if (lane == 0) mbar_arrive(&sh.mv_full[st]);
+            ++n;
+          }
+          more = wk.next(p);
+        }
+      }
     }
   } else if (warp >= kSoftWarps) {
     // ------------------------------------------------------------ dequantization
     regs_dec<kRegsDeq>();
     const int dw = warp - kSoftWarps, g = dw >> 1, half = dw & 1;
-    int it = 0, n = 0;
-    bool more = true;
+    const int pg = 32 * g / p.P, gp = g - pg * (p.P / 32);  // page of the tile, group of the page
+    int it = 0, n = 0;  // tiles whose keys are written; page tiles among them
+    bool more = true, ok = true, pend = false, phave = false;
+    // the values of the page tile before, whose record is in stage (n - 1) % kRecStages
+    auto values = [&](int j) {
+      if (j > 0) ok = wait_warp(sh, &sh.v_empty, uint32_t(j - 1) & 1u, p.err);
+      if (!ok) return;
+      const int st = (n - 1) % kRecStages;
+      if (phave)
+#pragma unroll 1
+        for (int a = 0; a < 2; ++a)
+          value_codes(p, smem + kRec + st * stage_bytes + pg * p.L.record, gp, g, half, a, smem, lane);
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.v_full);
+        mbar_arrive(&sh.rec_empty[st]);
+      }
+      pend = false;
+    };
     while (more) {
       const int v3 = it % 3;
       if (!wk.raw()) {
         const int st = n % kRecStages;
+        if (kMoves && !wait_warp(sh, &sh.mv_full[st], uint32_t(n / kRecStages) & 1u, p.err)) break;
         if (!wait_warp(sh, &sh.rec_full[st], uint32_t(n / kRecStages) & 1u, p.err)) break;
-        const int npg = min(PPT, wk.s.np - wk.k * PPT), pg = 32 * g / p.P, gp = g - pg * (p.P / 32);
-        const bool have = pg < npg;
+        const bool have = pg < wk.s.np - wk.k * PPT;
         const uint8_t* rec = smem + kRec + st * stage_bytes + pg * p.L.record;
-        int nm[4] = {0, 0, 0, 0};
-        if constexpr (KB > 0 && KB < 8)
-          if (have) boost_moves<KB>(rec + p.L.boost_idx, half, sh.tab[dw], nm, lane);
         if (it > 0 && !wait_warp(sh, &sh.k_empty, uint32_t(it - 1) & 1u, p.err)) break;
-        if (have) {
-          key_row<T, KB>(p, rec, 32 * gp + lane, 32 * g + lane, half, smem, sh.tab[dw], nm);
-          if (lane >= 16 && half == 0) {  // zero points: row 128 + g of the key operand
-            const int c = lane - 16, s = c >> 1, r = c & 1;
+        if (have)
+#pragma unroll 1
+          for (int a = 0; a < 2; ++a)
+            key_row<T, KB>(p, rec, 32 * gp + lane, 32 * g + lane, half, a, smem, sh.moves[kMoves ? st : 0][kMoves ? pg : 0]);
+        if (half == 0) {
+          if (have && lane < 16) {  // zero points: row 128 + g of the key operand
+            const int s = lane >> 1, r = lane & 1;
             const uint8_t* z = rec + p.L.k_zero + gp * 256 + (32 * (s >> 1) + 4 * (s & 1) + 2 * r) * 2;
             uint32_t x[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) x[q] = half_of(meta_h2(lds32(z + 16 * q), T()));
-            *reinterpret_cast<uint4*>(smem + kKhi + tco(128 + g, c)) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(smem + kKhi + tco(128 + g, lane)) = make_uint4(x[0], x[1], x[2], x[3]);
           }
-        }
-        if (half == 0) {
+        } else {
           float s = 0.0f, z = 0.0f;
           if (have) {
             const int at = 2 * value_meta_pos(32 * gp + lane);
@@ -581,84 +729,56 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             z = bits_to_float(*reinterpret_cast<const uint16_t*>(rec + p.L.v_zero + at), T());
           }
           sh.vs[v3][32 * g + lane] = s;
-          sh.vz[v3][32 * g + lane] = z;
+          sh.vz[v3][32 * g + lane] = fmaf(1.5f, s, z);
           const uint32_t mx = __reduce_max_sync(kFull, __float_as_uint(fabsf(s)));
           if (lane == 0) sh.smax[v3][g] = __uint_as_float(mx);
         }
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_full);
-        if (it > 0 && !wait_warp(sh, &sh.v_empty, uint32_t(it - 1) & 1u, p.err)) break;
-        if (have) value_codes(p, rec, gp, g, half, smem, lane);
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sh.v_full);
-          mbar_arrive(&sh.rec_empty[st]);
-        }
+        if (pend) values(it - 1);
+        if (!ok) break;
+        pend = true;
+        phave = have;
         ++n;
       } else {
-        // window and drafted tokens: warp dw takes tokens 16 dw .. 16 dw + 15 of the tile, two at a time
+        // window and drafted tokens: warp dw takes tokens 16 dw .. 16 dw + 15 of the tile, two at
+        // a time, 16 lanes a token
         const int x0 = 128 * (wk.k - wk.s.ntp), nx = wk.s.rl + wk.s.dl, c = lane & 15;
-        uint4 kx[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int x = x0 + 16 * dw + 2 * i + (lane >> 4);
-          kx[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (x < nx) {
-            bool draft;
-            const size_t at = raw_row(p, wk.b, wk.h, wk.s.rl, x, draft) + c;
-            kx[i] = __ldcg(reinterpret_cast<const uint4*>(draft ? p.k_draft : p.res_k) + at);
-          }
-        }
         if (it > 0 && !wait_warp(sh, &sh.k_empty, uint32_t(it - 1) & 1u, p.err)) break;
-#pragma unroll
+        float top = 0.0f;
+#pragma unroll 2
         for (int i = 0; i < 8; ++i) {
-          uint32_t* k = reinterpret_cast<uint32_t*>(&kx[i]);
+          const int t = 16 * dw + 2 * i + (lane >> 4), x = x0 + t;
+          bool draft = false, bad = false;
+          uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
+          if (x < nx) {
+            const size_t at = raw_row(p, wk.b, wk.h, wk.s.rl, x, draft) + c;
+            kx = __ldcg(reinterpret_cast<const uint4*>(draft ? p.k_draft : p.res_k) + at);
+            vx = __ldcg(reinterpret_cast<const uint4*>(draft ? p.v_draft : p.res_v) + at);
+          }
+          uint32_t k[4] = {kx.x, kx.y, kx.z, kx.w};
+          const uint32_t v[4] = {vx.x, vx.y, vx.z, vx.w};
+          float m = 0.0f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 f = unpack2(k[e], T());
             k[e] = pack_h2(0.5f * f.x, 0.5f * f.y);
+            const float2 y = unpack2(finite2(v[e], BF ? 0x7f80u : 0x7c00u, bad), T());
+            m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
           }
-          *reinterpret_cast<uint4*>(smem + kKhi + tco(16 * dw + 2 * i + (lane >> 4), c)) = kx[i];
-        }
-        // the values: finite, and for bf16 brought below 2 by a power of two of the token
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int x = x0 + 16 * dw + 2 * i + (lane >> 4);
-          kx[i] = make_uint4(0u, 0u, 0u, 0u);
-          bool draft = false, bad = false;
-          if (x < nx) {
-            const size_t at = raw_row(p, wk.b, wk.h, wk.s.rl, x, draft) + c;
-            kx[i] = __ldcg(reinterpret_cast<const uint4*>(draft ? p.v_draft : p.res_v) + at);
-          }
-          uint32_t* v = reinterpret_cast<uint32_t*>(&kx[i]);
-          float m = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = finite2(v[e], BF ? 0x7f80u : 0x7c00u, bad);
-            const float2 f = unpack2(v[e], T());
-            m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
+          *reinterpret_cast<uint4*>(smem + kKhi + tco(t, c)) = make_uint4(k[0], k[1], k[2], k[3]);
           if (bad && (!draft || seen_by_any(p, wk.b, wk.s.dl, x - wk.s.rl))) flag_error(p.err, KVQ_DEV_ERR_RANGE);
           float s = 0.5f;
-          if constexpr (BF) {
+          if constexpr (BF) {  // the power of two below the token's largest value
 #pragma unroll
             for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-            const int e = max(-100, min(100, int((__float_as_uint(m) >> 23) & 0xff) - 127));
-            const float f = pow2i(-e);
-            s = 0.5f * pow2i(e);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 y = unpack2(v[j], T());
-              v[j] = pack_h2(y.x * f, y.y * f);
-            }
+            s = 0.5f * pow2i(max(-90, min(100, int((__float_as_uint(m) >> 23) & 0xff) - 127)));
           }
           if (x >= nx) s = 0.0f;
           if (c == 0) {
-            sh.vs[v3][16 * dw + 2 * i + (lane >> 4)] = s;
-            sh.vz[v3][16 * dw + 2 * i + (lane >> 4)] = 0.0f;
+            sh.vs[v3][t] = s;
+            sh.vz[v3][t] = 0.0f;
           }
           top = fmaxf(top, s);
         }
@@ -667,10 +787,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_full);
+        if (pend) values(it - 1);
+        if (!ok) break;
+        // the values: what is no number is zero (a probability of zero has to stay zero), and
+        // bf16 is brought below 2 by the token's power of two
         if (it > 0 && !wait_warp(sh, &sh.v_empty, uint32_t(it - 1) & 1u, p.err)) break;
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+          const int t = 16 * dw + 2 * i + (lane >> 4), x = x0 + t;
+          uint4 vx = make_uint4(0u, 0u, 0u, 0u);
+          if (x < nx) {
+            bool draft;
+            const size_t at = raw_row(p, wk.b, wk.h, wk.s.rl, x, draft) + c;
+            vx = __ldcg(reinterpret_cast<const uint4*>(draft ? p.v_draft : p.res_v) + at);
+          }
+          uint32_t v[4] = {vx.x, vx.y, vx.z, vx.w};
+          bool bad = false;
+          const float f = BF ? 0.5f / fmaxf(sh.vs[v3][t], 1e-30f) : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(smem + kV + tco(16 * dw + 2 * i + (lane >> 4), c)) = kx[i];
+          for (int e = 0; e < 4; ++e) {
+            v[e] = finite2(v[e], BF ? 0x7f80u : 0x7c00u, bad);
+            if constexpr (BF) {
+              const float2 y = unpack2(v[e], T());
+              v[e] = pack_h2(y.x * f, y.y * f);
+            }
+          }
+          *reinterpret_cast<uint4*>(smem + kV + tco(t, c)) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.v_full);
@@ -678,141 +821,183 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       ++it;
       more = wk.next(p);
     }
+    if (!more && pend && ok) values(it - 1);
   } else {
     // ------------------------------------------------------------ softmax
     regs_inc<kRegsSoft>();
     const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
-    int it = 0, k0 = wk.k, u_dl = 0, u_rl = 0;
+    int it = 0, run = 0, k0 = 0;  // tiles; tiles of this part of the unit, and its first
+    bool valid = false, some = false, to_end = false;
+    int u_dl = 0, u_rl = 0;
+    size_t orow = 0;
     float M = -INFINITY, l = 0.0f, zs = 0.0f, cl = 0.0f;
     float asc = 0.0f;  // factor of the sums in shared memory against O (0: nothing there yet)
-    int run = 0;       // tiles of this part of the unit so far
     float4* acc = reinterpret_cast<float4*>(smem + kAcc) + 16 * half * 128 + row;  // [column / 4][row]
+    const uint32_t tO = tc::lane_addr(tm + kColO, warp, 64 * half);
     uint32_t mk[4] = {0u, 0u, 0u, 0u};  // drafted tokens this row sees
-    size_t orow = 0;
-    bool valid = false, some = false, more = true;
     // Waits until the second product of tile j is complete.  A parity names a phase only
     // among two: with a barrier for every other tile, and tile it - 2 waited for at tile it,
-    // the phase asked for is always the current one or the one before.
+    // the phase asked for is always the current one or the one before.  (After a wait that
+    // gave up every other one returns at once: the loop runs out by itself, and the pairs'
+    // barriers stay matched.)
     auto wait_pv = [&](int j) {
       wait(sh, &sh.pv_done[j & 1], uint32_t(j >> 1) & 1u, p.err);
       __syncwarp();
+      tc::fence_after();
     };
-    auto load_q = [&](const Walk& w) {
-      const int R = 128 * w.r + row, i = R / p.gqa;
-      valid = i < w.s.dl;
-      some = 128 * w.r + 32 * quarter < w.s.dl * p.gqa;  // any row of this warp
-      orow = (size_t(w.b) * p.T + i) * p.Hq + w.h * p.gqa + (R - i * p.gqa);
-      u_dl = w.s.dl;
-      u_rl = w.s.rl;
-      if (some) {
-        uint4 v[8];
+    bool done = false;
+    while (true) {
+      if (wk.first || done) {
+        // the unit before is complete but for its second products; first the next unit's query,
+        // so that its products start while these rows are written
+        const bool v0 = valid, some0 = some, whole = k0 == 0 && to_end;
+        float* dst = whole ? p.out + orow * kHeadDim : p.part + (size_t(2 * cta + (k0 == 0 ? 1 : 0)) * 128 + row) * kPart;
+        if (!done) {
+          const int R = 128 * wk.r + row, i = R / p.gqa;
+          valid = i < wk.s.dl;
+          some = 128 * wk.r + 32 * quarter < wk.s.dl * p.gqa;  // any row of this warp
+          orow = (size_t(wk.b) * p.T + i) * p.Hq + wk.h * p.gqa + (R - i * p.gqa);
+          u_dl = wk.s.dl;
+          u_rl = wk.s.rl;
+          if (some) {
+            uint32_t v[32];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[j] = valid ? __ldcg(reinterpret_cast<const uint4*>(p.q + orow * kHeadDim + 64 * half) + j)
-                       : make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < 8; ++j) {
+              const uint4 x = valid ? __ldcg(reinterpret_cast<const uint4*>(p.q + orow * kHeadDim + 64 * half) + j)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+              v[4 * j] = x.x;
+              v[4 * j + 1] = x.y;
+              v[4 * j + 2] = x.z;
+              v[4 * j + 3] = x.w;
+            }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          mk[j] = valid && j < p.W ? __ldcg(p.mask + (size_t(w.b) * p.T + i) * p.W + j) : 0u;
-          const int left = u_dl - 32 * j;
-          mk[j] &= left >= 32 ? kFull : left > 0 ? (1u << left) - 1u : 0u;
+            for (int j = 0; j < 4; ++j) {
+              mk[j] = valid && j < p.W ? __ldcg(p.mask + (size_t(wk.b) * p.T + i) * p.W + j) : 0u;
+              const int left = u_dl - 32 * j;
+              mk[j] &= left >= 32 ? kFull : left > 0 ? (1u << left) - 1u : 0u;
+            }
+            float m = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float2 f = unpack2(v[j], T());
+              m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            pair_sync(1 + quarter);
+            sh.xch[0][row][half] = m;
+            pair_sync(1 + quarter);
+            m = fmaxf(m, sh.xch[0][row][half ^ 1]);
+            pair_sync(1 + quarter);
+            // |q| < 2^e; e = 0 below 1
+            const int e = min(max(int((__float_as_uint(m) >> 23) & 0xff) - 126, 0), 126);
+            const float f = p.c_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
+            cl = 2.0f * fabsf(p.c_log2) * pow2i(e);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float2 y = unpack2(v[j], T());
+              v[j] = pack_h2(y.x * f, y.y * f);
+            }
+            tc::st<32>(tc::lane_addr(tm + kColQ, warp, 32 * half), v);
+            tc::wait_st();
+          }
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.q_full);
         }
-        float m = 0.0f;
+        if (it > 0) {
+          wait_pv(it - 1);
+          if (some0) {
+            pair_sync(1 + quarter);
+            sh.xch[0][row][half] = l;
+            sh.xch[1][row][half] = zs;
+            pair_sync(1 + quarter);
+            l += sh.xch[0][row][half ^ 1];
+            zs += sh.xch[1][row][half ^ 1];
+            pair_sync(1 + quarter);
+            const float inv = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+            bool bad = !(l < INFINITY);
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[16];
+              tc::ld<16>(tO + 16 * i, o);
+              wait_ld(o);
+              if (v0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 a = asc != 0.0f ? acc[(4 * i + j / 4) * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
+                  float x[4] = {fmaf(a.x, asc, __uint_as_float(o[j])), fmaf(a.y, asc, __uint_as_float(o[j + 1])),
+                                fmaf(a.z, asc, __uint_as_float(o[j + 2])), fmaf(a.w, asc, __uint_as_float(o[j + 3]))};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack2(x[e], T());
-            m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+                  for (int e = 0; e < 4; ++e) {
+                    x[e] = fmaf(2.0f, x[e], zs) * inv;
+                    bad |= !(fabsf(x[e]) < INFINITY);
+                  }
+                  *reinterpret_cast<float4*>(dst + 64 * half + 16 * i + j) = make_float4(x[0], x[1], x[2], x[3]);
+                }
+              }
+            }
+            if (v0) {
+              if (bad) flag_error(p.err, KVQ_DEV_ERR_RANGE);
+              if (!whole && half == 0) {
+                dst[128] = M;
+                dst[129] = l;
+              }
+            }
           }
         }
-        pair_sync(1 + quarter);
-        sh.xch[0][row][half] = m;
-        pair_sync(1 + quarter);
-        m = fmaxf(m, sh.xch[0][row][half ^ 1]);
-        pair_sync(1 + quarter);
-        // |q| < 2^e; e = 0 below 1
-        const int e = min(max(int((__float_as_uint(m) >> 23) & 0xff) - 126, 0), 126);
-        const float f = p.c_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
-        cl = 2.0f * fabsf(p.c_log2) * pow2i(e);
-        uint32_t qh[32];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float2 y = unpack2(x[c], T());
-            qh[4 * j + c] = pack_h2(y.x * f, y.y * f);
-          }
-        }
-        tc::st<32>(tc::lane_addr(tm + kColQ, warp, 32 * half), qh);
-        tc::wait_st();
+        if (done) break;
+        M = -INFINITY;
+        l = zs = asc = 0.0f;
+        run = 0;
+        k0 = wk.k;
       }
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.q_full);
-    };
-    load_q(wk);
-    while (more) {
       const int buf = it & 1, v3 = it % 3;
-      const uint32_t tS = tm + uint32_t(buf) * kColS;
+      const uint32_t tS = tm + uint32_t(buf) * kColS, tR = tc::lane_addr(tS, warp, 64 * half);
       const bool raw = wk.raw();
-      // (after a wait that gave up every other one returns at once: the loop runs out by
-      // itself, and the pairs' barriers stay matched)
       wait(sh, &sh.s_full[buf], uint32_t(it >> 1) & 1u, p.err);
       if (it >= 2) wait_pv(it - 2);
       __syncwarp();
       tc::fence_after();
       if (some) {
-        uint32_t sv[4][16], zr[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tc::ld<16>(tc::lane_addr(tS, warp, 64 * half + 16 * i), sv[i]);
-        if (!raw) tc::ld<2>(tc::lane_addr(tS, warp, 128 + 2 * half), zr);
-        tc::wait_ld();
-        float zb[2] = {__uint_as_float(zr[0]) * cl, __uint_as_float(zr[1]) * cl};
-        float mx = -INFINITY;
+        // first pass: the largest logit of this half (S is read again for the second)
+        float zb0 = 0.0f, zb1 = 0.0f, m0, m1;
+        uint32_t see0 = kFull, see1 = kFull;
         if (!raw) {
-          const int ng = (wk.s.np - wk.k * PPT) * (p.P / 32);  // groups of the tile that hold tokens (4 or more: all)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float a = __uint_as_float(sv[2 * i][0]);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) a = fmaxf(a, __uint_as_float(sv[2 * i + (j >> 4)][j & 15]));
-            if (2 * half + i < ng) {
-              mx = fmaxf(mx, fmaf(a, cl, zb[i]));
-            } else {
-              zb[i] = -INFINITY;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) sv[2 * i + (j >> 4)][j & 15] = 0u;
-            }
-          }
+          uint32_t zr[2];
+          tc::ld<2>(tc::lane_addr(tS, warp, 128 + 2 * half), zr);
+          const int ng = (wk.s.np - wk.k * PPT) * (p.P / 32) - 2 * half;  // groups of this half that hold tokens (2 or more: all)
+          see0 = ng > 0 ? kFull : 0u;
+          see1 = ng > 1 ? kFull : 0u;
+          m0 = largest<false>(tR, kFull);
+          m1 = largest<false>(tR + 32, kFull);
+          asm volatile("" : "+r"(zr[0]), "+r"(zr[1]));
+          zb0 = __uint_as_float(zr[0]) * cl;
+          zb1 = __uint_as_float(zr[1]) * cl;
         } else {
-          // bit j of vis[i]: the row sees token 32 i + j of its half
+          // bit j of see0, see1: the row sees token j, 32 + j of its half
           const int x0 = 128 * (wk.k - wk.s.ntp) + 64 * half;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int xw = x0 + 32 * i, in_window = u_rl - xw, d = xw - u_rl;  // first drafted token of the word
-            uint32_t vis = in_window >= 32 ? kFull : in_window > 0 ? (1u << in_window) - 1u : 0u;
+          auto sees = [&](int xw) {
+            const int in_window = u_rl - xw, d = xw - u_rl;  // d: first drafted token of the word
+            uint32_t v = in_window >= 32 ? kFull : in_window > 0 ? (1u << in_window) - 1u : 0u;
             if (d > -32) {
               const int wd = d >> 5;
-              uint32_t a = 0u, b2 = 0u;
+              uint32_t a = 0u, b = 0u;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 a = j == wd ? mk[j] : a;
-                b2 = j == wd + 1 ? mk[j] : b2;
+                b = j == wd + 1 ? mk[j] : b;
               }
-              vis |= __funnelshift_r(a, b2, uint32_t(d) & 31u);
+              v |= __funnelshift_r(a, b, uint32_t(d) & 31u);
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              uint32_t& s = sv[2 * i + (j >> 4)][j & 15];
-              s = ((vis >> j) & 1u) ? __float_as_uint(__uint_as_float(s) * cl) : 0xff800000u;
-              mx = fmaxf(mx, __uint_as_float(s));
-            }
-          }
+            return v;
+          };
+          see0 = sees(x0);
+          see1 = sees(x0 + 32);
+          m0 = largest<true>(tR, see0);
+          m1 = largest<true>(tR + 32, see1);
         }
+        float mx = fmaxf(see0 ? fmaf(m0, cl, zb0) : -INFINITY, see1 ? fmaf(m1, cl, zb1) : -INFINITY);
         sh.xch[buf][row][half] = mx;
-        pair_sync(1 + quarter);  // also: both threads of the row have read S
+        pair_sync(1 + quarter);
         mx = fmaxf(mx, sh.xch[buf][row][half ^ 1]);
         float sm;
         if (!raw) {
@@ -833,144 +1018,45 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           asc *= alpha;
           M = mx;
         }
-        if (run > 0 && run % kFlush == 0) {
-          // O into the sums; it starts anew with this tile
+        const bool flush = run > 0 && run % kFlush == 0;
+        if (flush || (run > 0 && __any_sync(kFull, alpha != 1.0f))) {
+          // O into the sums, to start anew with this tile; or only to the new reference
           wait_pv(it - 1);
-          tc::fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             uint32_t o[16];
-            tc::ld<16>(tc::lane_addr(tm + kColO, warp, 64 * half + 16 * i), o);
-            tc::wait_ld();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float4& a = acc[(4 * i + j) * 128];
-              float4 x = asc != 0.0f ? a : make_float4(0.f, 0.f, 0.f, 0.f);
-              x.x = fmaf(x.x, asc, __uint_as_float(o[4 * j]) * alpha);
-              x.y = fmaf(x.y, asc, __uint_as_float(o[4 * j + 1]) * alpha);
-              x.z = fmaf(x.z, asc, __uint_as_float(o[4 * j + 2]) * alpha);
-              x.w = fmaf(x.w, asc, __uint_as_float(o[4 * j + 3]) * alpha);
-              a = x;
-            }
-          }
-          asc = 1.0f;
-        } else if (run > 0 && __any_sync(kFull, alpha != 1.0f)) {
-          wait_pv(it - 1);
-          tc::fence_after();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[16];
-            tc::ld<16>(tc::lane_addr(tm + kColO, warp, 64 * half + 16 * i), o);
-            tc::wait_ld();
+            tc::ld<16>(tO + 16 * i, o);
+            wait_ld(o);
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-            tc::st<16>(tc::lane_addr(tm + kColO, warp, 64 * half + 16 * i), o);
-          }
-        }
-        const float nm = M == -INFINITY ? 0.0f : 7.0f - M;
-        const float mul = raw ? 1.0f : cl;
-        float lp[4] = {0.0f, 0.0f, 0.0f, 0.0f}, zp[2] = {0.0f, 0.0f};
+            if (flush) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // 16 tokens: 8 columns of high parts, 8 of low parts
-          const float off = raw ? nm : zb[i >> 1] + nm;
-          uint32_t ph[8], pl[8];
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 s4 = *reinterpret_cast<const float4*>(&sh.vs[v3][64 * half + 16 * i + j]);
-            const float4 z4 = *reinterpret_cast<const float4*>(&sh.vz[v3][64 * half + 16 * i + j]);
-            float pr[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pr[e] = ex2(__fmaf_rn(__uint_as_float(sv[i][j + e]), mul, off));
-            lp[i] += (pr[0] + pr[1]) + (pr[2] + pr[3]);
-            zp[0] = fmaf(pr[0], z4.x, zp[0]);
-            zp[1] = fmaf(pr[1], z4.y, zp[1]);
-            zp[0] = fmaf(pr[2], z4.z, zp[0]);
-            zp[1] = fmaf(pr[3], z4.w, zp[1]);
-            pr[0] *= s4.x;
-            pr[1] *= s4.y;
-            pr[2] *= s4.z;
-            pr[3] *= s4.w;
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              const uint32_t hp = pack_h2(pr[e], pr[e + 1]);
-              const float2 hf = __half22float2(u32_as_h2(hp));
-              ph[(j + e) / 2] = hp;
-              pl[(j + e) / 2] = pack_h2(pr[e] - hf.x, pr[e + 1] - hf.y);
+              for (int j = 0; j < 4; ++j) {
+                float4& a = acc[(4 * i + j) * 128];
+                const float4 x = asc != 0.0f ? a : make_float4(0.f, 0.f, 0.f, 0.f);
+                a = make_float4(fmaf(x.x, asc, __uint_as_float(o[4 * j])), fmaf(x.y, asc, __uint_as_float(o[4 * j + 1])),
+                                fmaf(x.z, asc, __uint_as_float(o[4 * j + 2])), fmaf(x.w, asc, __uint_as_float(o[4 * j + 3])));
+              }
+            } else {
+              tc::st<16>(tO + 16 * i, o);
             }
           }
-          tc::st<8>(tc::lane_addr(tS, warp, 32 * half + 8 * i), ph);
-          tc::st<8>(tc::lane_addr(tS, warp, 64 + 32 * half + 8 * i), pl);
+          if (flush) asc = 1.0f;
         }
-        l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
-        zs += zp[0] + zp[1];
+        // second pass; a group without tokens holds old sums, which may be no number
+        const float nm = M == -INFINITY ? 0.0f : 7.0f - M;
+        const float *vs = &sh.vs[v3][64 * half], *vz = &sh.vz[v3][64 * half];
+        if (raw || see1 == 0u)
+          weights<true>(tR, cl, zb0 + nm, zb1 + nm, see0, see1, vs, vz, l, zs);
+        else
+          weights<false>(tR, cl, zb0 + nm, zb1 + nm, kFull, kFull, vs, vz, l, zs);
         tc::wait_st();
       }
       tc::fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_full[buf]);
-
-      const bool last = wk.last, from0 = k0 == 0, to_end = wk.k == wk.s.nt - 1;
-      more = wk.next(p);
-      if (last) {
-        // what this unit's rows need, before the next unit's query replaces it
-        const bool v0 = valid, some0 = some;
-        const size_t out_row = orow;
-        const float M0 = M;
-        float l0 = l, z0 = zs;
-        if (more) load_q(wk);
-        wait_pv(it);
-        tc::fence_after();
-        if (some0) {
-          pair_sync(1 + quarter);
-          sh.xch[0][row][half] = l0;
-          sh.xch[1][row][half] = z0;
-          pair_sync(1 + quarter);
-          l0 += sh.xch[0][row][half ^ 1];
-          z0 += sh.xch[1][row][half ^ 1];
-          pair_sync(1 + quarter);
-          const bool whole = from0 && to_end;
-          const float inv = whole ? (l0 > 0.0f ? 1.0f / l0 : 0.0f) : 1.0f;
-          float* dst = whole ? p.out + out_row * kHeadDim
-                             : p.part + (size_t(2 * cta + (from0 ? 1 : 0)) * 128 + row) * kPart;
-          bool bad = false;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[16];
-            tc::ld<16>(tc::lane_addr(tm + kColO, warp, 64 * half + 16 * i), o);
-            tc::wait_ld();
-            if (v0) {
-#pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                if (asc != 0.0f) {
-                  const float4 a = acc[(4 * i + j / 4) * 128];
-                  o[j] = __float_as_uint(fmaf(a.x, asc, __uint_as_float(o[j])));
-                  o[j + 1] = __float_as_uint(fmaf(a.y, asc, __uint_as_float(o[j + 1])));
-                  o[j + 2] = __float_as_uint(fmaf(a.z, asc, __uint_as_float(o[j + 2])));
-                  o[j + 3] = __float_as_uint(fmaf(a.w, asc, __uint_as_float(o[j + 3])));
-                }
-                float x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  x[e] = fmaf(2.0f, __uint_as_float(o[j + e]), z0) * inv;
-                  bad |= !(fabsf(x[e]) < INFINITY);
-                }
-                *reinterpret_cast<float4*>(dst + 64 * half + 16 * i + j) = make_float4(x[0], x[1], x[2], x[3]);
-              }
-            }
-          }
-          if (v0) {
-            if (bad || !(l0 < INFINITY)) flag_error(p.err, KVQ_DEV_ERR_RANGE);
-            if (!whole && half == 0) {
-              dst[128] = M0;
-              dst[129] = l0;
-            }
-          }
-        }
-        M = -INFINITY;
-        l = zs = asc = 0.0f;
-        run = -1;
-        k0 = more ? wk.k : 0;
-      }
+      to_end = wk.k == wk.s.nt - 1;
+      done = !wk.next(p);
       ++it;
       ++run;
     }
