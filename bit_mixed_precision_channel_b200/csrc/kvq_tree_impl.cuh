@@ -18,8 +18,8 @@
 //   dequant    8 warps   write the keys of a tile, then the value codes of the tile before,
 //                        as fp16 operands;
 //   issuer     1 warp    S = Q K^T, then O += P V of the tile before (tcgen05, M = 128);
-//   softmax    8 warps   a thread per (row, half of the tile's tokens): S from tensor
-//                        memory, running maximum, P back over S.
+//   softmax    8 warps   16 rows each, four lanes a row: S from tensor memory, running
+//                        maximum, P back over S.
 // Two S / P buffers of 144 columns, O (128 columns) and Q (64 columns) fill tensor memory.
 //
 // Arithmetic.  Everything is carried to about 22 bits, as the decode kernel does, so that a
@@ -62,9 +62,10 @@ constexpr int kRecStages = 3;
 // memory, which round to nearest.  (Left in tensor memory over 28 tiles of a 4096-token
 // cache, the output was off by 3.6e-5 against 64 bits.)
 constexpr int kFlush = 4;
+constexpr uint32_t kAccStride = 132 * 8;  // output sums: [column / 2][row], rows padded against bank conflicts
 // shared-memory offsets: key operand (high parts and zero points, remainders), value operand,
 // output sums, record stages
-constexpr uint32_t kKhi = 0, kKlo = 144 * 256, kV = kKlo + 128 * 256, kAcc = kV + 128 * 256, kRec = kAcc + 128 * 512;
+constexpr uint32_t kKhi = 0, kKlo = 144 * 256, kV = kKlo + 128 * 256, kAcc = kV + 128 * 256, kRec = kAcc + 64 * kAccStride;
 constexpr int kColS = 144, kColO = 288, kColQ = 416;  // tensor-memory columns: S at 0 and 144
 
 __device__ __forceinline__ uint32_t tco(int r, int c) { return uint32_t((r >> 3) * 2048 + c * 128 + (r & 7) * 16); }
@@ -81,13 +82,46 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(x));
   return x != 0;
 }
-// Waits for this thread's tensor-memory loads; naming the registers keeps their uses behind it.
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
+// Tensor memory of the 16 lanes at `a`, as the matrix instructions of a warp lay a tile out:
+// lane i of the warp holds rows i / 4 and i / 4 + 8.  ld32: 32 columns of 32 bits, columns
+// 8 c + 2 (i % 4) and the next in r[4 c], r[4 c + 1] (row i / 4) and r[4 c + 2], r[4 c + 3].
+// The loads are complete on return: the wait names the registers, which keeps uses behind it.
+__device__ __forceinline__ void ld32(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a)
+      : "memory");
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
                  "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void st32(uint32_t a, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// 4 columns: column i % 4 of rows i / 4 and i / 4 + 8.
+__device__ __forceinline__ void ld4(uint32_t a, uint32_t (&r)[2]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x128b.x1.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1])::"memory");
+}
+// 8 columns: column 4 c + i % 4 in r[2 c] (row i / 4) and r[2 c + 1].
+__device__ __forceinline__ void st8(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
+  return fmaxf(x, __shfl_xor_sync(kFull, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(kFull, x, 1);
+  return x + __shfl_xor_sync(kFull, x, 2);
+}
 
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -244,9 +278,8 @@ struct Shared {
       p_full[2], pv_done[2], q_full;
   uint32_t tmem;
   int abort;
-  float xch[2][128][2];                 // [parity][row][half]
-  __align__(16) float vs[3][128];       // value scale (raw tiles: 2^e_t / 2) of a tile's tokens
-  __align__(16) float vz[3][128];       // value zero point + 1.5 scales
+  // value scale s (raw tiles: 2^e_t / 2) and zero point + 1.5 s of two tokens {s, s', z, z'}
+  float4 sz[3][64];
   float smax[3][4];                     // largest value scale of a page tile's groups
   float xs[3][kDeqWarps];               // the same of a raw tile, by the warp that wrote it
   Line line;
@@ -437,77 +470,61 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x, uint32_t expo, bool& bad
 
 // ---------------------------------------------------------------- softmax
 
-// The 64 logits of one row at tensor-memory columns tR .. tR + 63 into probabilities
-// 2^(cl S + off) (off0 for the first 32 tokens, off1 for the others; 0 where the token's bit
-// of see0 / see1 is clear), times the tokens' value scales, as fp16 high and low parts in the
-// same columns: 16 tokens in 8 + 8.  Adds their sum to l and their sum with vz to zs.
-// MASK: whether the bits differ within a word.
+// 32 logits of the lane's two rows at columns tR .. tR + 31, as 2^(cl S + off), 0 where the
+// token's bit of see is clear (MASK), times the tokens' value scales, back in the same columns
+// as fp16 high and low parts: every 16 tokens in 8 + 8 columns.  sz: {s, s', z, z'} of the
+// tokens' pairs, from the lane's first on.  The sums (also with z) go to l and zs.
 template <bool MASK>
-__device__ __forceinline__ void weights(uint32_t tR, float cl, float off0, float off1, uint32_t see0, uint32_t see1,
-                                        const float* vs, const float* vz, float& l, float& zs) {
-  float lp[4] = {0.0f, 0.0f, 0.0f, 0.0f}, zp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
-    uint32_t sx[16];
-    tc::ld<16>(tR + 16 * i, sx);
-    const float off = i < 2 ? off0 : off1;
-    const uint32_t see = (i < 2 ? see0 : see1) >> (16 * (i & 1));
-    wait_ld(sx);
-    uint32_t ph[8], pl[8];
-    float pr[16];
+__device__ __forceinline__ void weights(uint32_t tR, const float (&cl)[2], const float (&off)[2], const uint32_t (&see)[2],
+                                        const float4* sz, float (&l)[2], float (&zs)[2]) {
+  uint32_t x[16];
+  ld32(tR, x);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      pr[j] = ex2(__fmaf_rn(__uint_as_float(sx[j]), cl, off));
-      if (MASK) pr[j] = ((see >> j) & 1u) ? pr[j] : 0.0f;
+  for (int c = 0; c < 4; c += 2) {  // 16 tokens
+    uint32_t hi[2][2], lo[2][2];    // [8 tokens][row]
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      const float4 v = sz[4 * (c + d)];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float p0 = ex2(__fmaf_rn(__uint_as_float(x[4 * (c + d) + 2 * r]), cl[r], off[r]));
+        float p1 = ex2(__fmaf_rn(__uint_as_float(x[4 * (c + d) + 2 * r + 1]), cl[r], off[r]));
+        if (MASK) {  // see is shifted to the lane's first token
+          p0 = (see[r] >> (8 * (c + d))) & 1u ? p0 : 0.0f;
+          p1 = (see[r] >> (8 * (c + d) + 1)) & 1u ? p1 : 0.0f;
+        }
+        l[r] += p0 + p1;
+        zs[r] = fmaf(p0, v.z, zs[r]);
+        zs[r] = fmaf(p1, v.w, zs[r]);
+        p0 *= v.x;
+        p1 *= v.y;
+        const uint32_t h = pack_h2(p0, p1);
+        const float2 f = __half22float2(u32_as_h2(h));
+        hi[d][r] = h;
+        lo[d][r] = pack_h2(p0 - f.x, p1 - f.y);
+      }
     }
-#pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-      const float4 s4 = *reinterpret_cast<const float4*>(vs + 16 * i + j);
-      const float4 z4 = *reinterpret_cast<const float4*>(vz + 16 * i + j);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) lp[e] += pr[j + e];
-      zp[0] = fmaf(pr[j], z4.x, zp[0]);
-      zp[1] = fmaf(pr[j + 1], z4.y, zp[1]);
-      zp[2] = fmaf(pr[j + 2], z4.z, zp[2]);
-      zp[3] = fmaf(pr[j + 3], z4.w, zp[3]);
-      pr[j] *= s4.x;
-      pr[j + 1] *= s4.y;
-      pr[j + 2] *= s4.z;
-      pr[j + 3] *= s4.w;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      ph[j] = pack_h2(pr[2 * j], pr[2 * j + 1]);
-      const float2 hf = __half22float2(u32_as_h2(ph[j]));
-      pl[j] = pack_h2(pr[2 * j] - hf.x, pr[2 * j + 1] - hf.y);
-    }
-    tc::st<8>(tR + 16 * i, ph);
-    tc::st<8>(tR + 16 * i + 8, pl);
+    st8(tR + 8 * c, hi[0][0], hi[0][1], hi[1][0], hi[1][1]);
+    st8(tR + 8 * c + 8, lo[0][0], lo[0][1], lo[1][0], lo[1][1]);
   }
-  l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
-  zs += (zp[0] + zp[1]) + (zp[2] + zp[3]);
 }
 
-// The largest of the 32 values at tensor-memory columns tR .. tR + 31 whose bit of see is set
-// (MASK), -inf if there is none; masked values may be no number.
+// The largest of the lane's logits S among 32 columns whose bit of see is set (MASK), -inf if
+// there is none; masked values may be no number.
 template <bool MASK>
-__device__ __forceinline__ float largest(uint32_t tR, uint32_t see) {
-  float m = -INFINITY;
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    uint32_t x[16];
-    tc::ld<16>(tR + 16 * i, x);
-    wait_ld(x);
+__device__ __forceinline__ void largest(uint32_t tR, const uint32_t (&see)[2], float (&m)[2]) {
+  uint32_t x[16];
+  ld32(tR, x);
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
     float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      a = fmaxf(a, !MASK || ((see >> j) & 1u) ? __uint_as_float(x[j]) : -INFINITY);
-      b = fmaxf(b, !MASK || ((see >> (j + 1)) & 1u) ? __uint_as_float(x[j + 1]) : -INFINITY);
+    for (int c = 0; c < 4; ++c) {
+      a = fmaxf(a, !MASK || ((see[r] >> (8 * c)) & 1u) ? __uint_as_float(x[4 * c + 2 * r]) : -INFINITY);
+      b = fmaxf(b, !MASK || ((see[r] >> (8 * c + 1)) & 1u) ? __uint_as_float(x[4 * c + 2 * r + 1]) : -INFINITY);
     }
-    m = fmaxf(m, fmaxf(a, b));
-    see >>= 16;
+    m[r] = fmaxf(a, b);
   }
-  return m;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -728,8 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             s = bits_to_float(*reinterpret_cast<const uint16_t*>(rec + p.L.v_scale + at), T());
             z = bits_to_float(*reinterpret_cast<const uint16_t*>(rec + p.L.v_zero + at), T());
           }
-          sh.vs[v3][32 * g + lane] = s;
-          sh.vz[v3][32 * g + lane] = fmaf(1.5f, s, z);
+          float* sz = reinterpret_cast<float*>(sh.sz[v3]) + 4 * (16 * g + (lane >> 1)) + (lane & 1);
+          sz[0] = s;
+          sz[2] = fmaf(1.5f, s, z);
           const uint32_t mx = __reduce_max_sync(kFull, __float_as_uint(fabsf(s)));
           if (lane == 0) sh.smax[v3][g] = __uint_as_float(mx);
         }
@@ -777,8 +795,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
           if (x >= nx) s = 0.0f;
           if (c == 0) {
-            sh.vs[v3][t] = s;
-            sh.vz[v3][t] = 0.0f;
+            float* sz = reinterpret_cast<float*>(sh.sz[v3]) + 4 * (t >> 1) + (t & 1);
+            sz[0] = s;
+            sz[2] = 0.0f;
           }
           top = fmaxf(top, s);
         }
@@ -803,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
           uint32_t v[4] = {vx.x, vx.y, vx.z, vx.w};
           bool bad = false;
-          const float f = BF ? 0.5f / fmaxf(sh.vs[v3][t], 1e-30f) : 1.0f;
+          const float f = BF ? 0.5f / fmaxf(reinterpret_cast<const float*>(sh.sz[v3])[4 * (t >> 1) + (t & 1)], 1e-30f) : 1.0f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             v[e] = finite2(v[e], BF ? 0x7f80u : 0x7c00u, bad);
@@ -825,78 +844,83 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   } else {
     // ------------------------------------------------------------ softmax
     regs_inc<kRegsSoft>();
-    const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+    const int row0 = 32 * (warp & 3) + 16 * (warp >> 2), quad = lane & 3;  // of the warp's rows the first; the lane's place
+    const int row = row0 + (lane >> 2);                                    // ... and row + 8
+    const uint32_t at = uint32_t(row0) << 16;                              // the warp's tensor-memory lanes
     int it = 0, run = 0, k0 = 0;  // tiles; tiles of this part of the unit, and its first
-    bool valid = false, some = false, to_end = false;
+    bool some = false, to_end = false;
+    bool valid[2] = {false, false};
     int u_dl = 0, u_rl = 0;
-    size_t orow = 0;
-    float M = -INFINITY, l = 0.0f, zs = 0.0f, cl = 0.0f;
-    float asc = 0.0f;  // factor of the sums in shared memory against O (0: nothing there yet)
-    float4* acc = reinterpret_cast<float4*>(smem + kAcc) + 16 * half * 128 + row;  // [column / 4][row]
-    const uint32_t tO = tc::lane_addr(tm + kColO, warp, 64 * half);
-    uint32_t mk[4] = {0u, 0u, 0u, 0u};  // drafted tokens this row sees
+    size_t orow[2] = {0, 0};
+    float M[2], l[2], zs[2], cl[2];
+    float asc[2];     // factor of the sums in shared memory against O (0: nothing there yet)
+    uint4 mk0, mk1;   // drafted tokens the rows see
     // Waits until the second product of tile j is complete.  A parity names a phase only
     // among two: with a barrier for every other tile, and tile it - 2 waited for at tile it,
     // the phase asked for is always the current one or the one before.  (After a wait that
-    // gave up every other one returns at once: the loop runs out by itself, and the pairs'
-    // barriers stay matched.)
+    // gave up every other one returns at once, and the loop runs out by itself.)
     auto wait_pv = [&](int j) {
       wait(sh, &sh.pv_done[j & 1], uint32_t(j >> 1) & 1u, p.err);
       __syncwarp();
       tc::fence_after();
+    };
+    auto sums = [&](int c2, int r) -> float2& {  // output sums of columns 2 c2, 2 c2 + 1
+      return *reinterpret_cast<float2*>(smem + kAcc + c2 * kAccStride + (row + 8 * r) * 8);
     };
     bool done = false;
     while (true) {
       if (wk.first || done) {
         // the unit before is complete but for its second products; first the next unit's query,
         // so that its products start while these rows are written
-        const bool v0 = valid, some0 = some, whole = k0 == 0 && to_end;
-        float* dst = whole ? p.out + orow * kHeadDim : p.part + (size_t(2 * cta + (k0 == 0 ? 1 : 0)) * 128 + row) * kPart;
+        const bool some0 = some, whole = k0 == 0 && to_end;
+        const bool v0[2] = {valid[0], valid[1]};
+        float* dst[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          dst[r] = whole ? p.out + orow[r] * kHeadDim
+                         : p.part + (size_t(2 * cta + (k0 == 0 ? 1 : 0)) * 128 + row + 8 * r) * kPart;
+        float ncl[2] = {0.0f, 0.0f};
         if (!done) {
-          const int R = 128 * wk.r + row, i = R / p.gqa;
-          valid = i < wk.s.dl;
-          some = 128 * wk.r + 32 * quarter < wk.s.dl * p.gqa;  // any row of this warp
-          orow = (size_t(wk.b) * p.T + i) * p.Hq + wk.h * p.gqa + (R - i * p.gqa);
+          some = 128 * wk.r + row0 < wk.s.dl * p.gqa;  // any row of this warp
           u_dl = wk.s.dl;
           u_rl = wk.s.rl;
           if (some) {
-            uint32_t v[32];
+            uint32_t v[32];  // [8 channels][row]: channels 2 quad, 2 quad + 1
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint4 x = valid ? __ldcg(reinterpret_cast<const uint4*>(p.q + orow * kHeadDim + 64 * half) + j)
-                                    : make_uint4(0u, 0u, 0u, 0u);
-              v[4 * j] = x.x;
-              v[4 * j + 1] = x.y;
-              v[4 * j + 2] = x.z;
-              v[4 * j + 3] = x.w;
+            for (int r = 0; r < 2; ++r) {
+              const int R = 128 * wk.r + row + 8 * r, i = R / p.gqa;
+              valid[r] = i < wk.s.dl;
+              orow[r] = (size_t(wk.b) * p.T + i) * p.Hq + wk.h * p.gqa + (R - i * p.gqa);
+              const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + orow[r] * kHeadDim) + quad;
+              float m = 0.0f;
+#pragma unroll
+              for (int c = 0; c < 16; ++c) v[2 * c + r] = valid[r] ? __ldcg(src + 4 * c) : 0u;
+              auto mask = [&](int j) {
+                const int left = u_dl - 32 * j;
+                return valid[r] && left > 0 ? __ldcg(p.mask + (size_t(wk.b) * p.T + i) * p.W + j) &
+                                                  (left >= 32 ? kFull : (1u << left) - 1u)
+                                            : 0u;
+              };
+              (r ? mk1 : mk0) = make_uint4(mask(0), mask(1), mask(2), mask(3));
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float2 f = unpack2(v[2 * c + r], T());
+                m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
+              m = quad_max(m);
+              // |q| < 2^e; e = 0 below 1
+              const int e = min(max(int((__float_as_uint(m) >> 23) & 0xff) - 126, 0), 126);
+              const float f = p.c_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
+              ncl[r] = 2.0f * fabsf(p.c_log2) * pow2i(e);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float2 y = unpack2(v[2 * c + r], T());
+                v[2 * c + r] = pack_h2(y.x * f, y.y * f);
+              }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mk[j] = valid && j < p.W ? __ldcg(p.mask + (size_t(wk.b) * p.T + i) * p.W + j) : 0u;
-              const int left = u_dl - 32 * j;
-              mk[j] &= left >= 32 ? kFull : left > 0 ? (1u << left) - 1u : 0u;
-            }
-            float m = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float2 f = unpack2(v[j], T());
-              m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-            pair_sync(1 + quarter);
-            sh.xch[0][row][half] = m;
-            pair_sync(1 + quarter);
-            m = fmaxf(m, sh.xch[0][row][half ^ 1]);
-            pair_sync(1 + quarter);
-            // |q| < 2^e; e = 0 below 1
-            const int e = min(max(int((__float_as_uint(m) >> 23) & 0xff) - 126, 0), 126);
-            const float f = p.c_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
-            cl = 2.0f * fabsf(p.c_log2) * pow2i(e);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float2 y = unpack2(v[j], T());
-              v[j] = pack_h2(y.x * f, y.y * f);
-            }
-            tc::st<32>(tc::lane_addr(tm + kColQ, warp, 32 * half), v);
+            for (int c = 0; c < 16; c += 2)
+              st8(tm + kColQ + at + 4 * c, v[2 * c], v[2 * c + 1], v[2 * c + 2], v[2 * c + 3]);
             tc::wait_st();
           }
           tc::fence_before();
@@ -906,99 +930,92 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (it > 0) {
           wait_pv(it - 1);
           if (some0) {
-            pair_sync(1 + quarter);
-            sh.xch[0][row][half] = l;
-            sh.xch[1][row][half] = zs;
-            pair_sync(1 + quarter);
-            l += sh.xch[0][row][half ^ 1];
-            zs += sh.xch[1][row][half ^ 1];
-            pair_sync(1 + quarter);
-            const float inv = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
-            bool bad = !(l < INFINITY);
+            float inv[2];
+            bool bad = false;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              l[r] = quad_sum(l[r]);
+              zs[r] = quad_sum(zs[r]);
+              inv[r] = whole ? (l[r] > 0.0f ? 1.0f / l[r] : 0.0f) : 1.0f;
+              bad |= v0[r] && !(l[r] < INFINITY);
+            }
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
               uint32_t o[16];
-              tc::ld<16>(tO + 16 * i, o);
-              wait_ld(o);
-              if (v0) {
+              ld32(tm + kColO + at + 32 * i, o);
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                  const float4 a = asc != 0.0f ? acc[(4 * i + j / 4) * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
-                  float x[4] = {fmaf(a.x, asc, __uint_as_float(o[j])), fmaf(a.y, asc, __uint_as_float(o[j + 1])),
-                                fmaf(a.z, asc, __uint_as_float(o[j + 2])), fmaf(a.w, asc, __uint_as_float(o[j + 3]))};
+              for (int c = 0; c < 4; ++c)
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    x[e] = fmaf(2.0f, x[e], zs) * inv;
-                    bad |= !(fabsf(x[e]) < INFINITY);
-                  }
-                  *reinterpret_cast<float4*>(dst + 64 * half + 16 * i + j) = make_float4(x[0], x[1], x[2], x[3]);
+                for (int r = 0; r < 2; ++r) {
+                  if (!v0[r]) continue;
+                  const float2 a = asc[r] != 0.0f ? sums(16 * i + 4 * c + quad, r) : make_float2(0.f, 0.f);
+                  const float x = fmaf(2.0f, fmaf(a.x, asc[r], __uint_as_float(o[4 * c + 2 * r])), zs[r]) * inv[r];
+                  const float y = fmaf(2.0f, fmaf(a.y, asc[r], __uint_as_float(o[4 * c + 2 * r + 1])), zs[r]) * inv[r];
+                  bad |= !(fabsf(x) < INFINITY) || !(fabsf(y) < INFINITY);
+                  *reinterpret_cast<float2*>(dst[r] + 32 * i + 8 * c + 2 * quad) = make_float2(x, y);
                 }
-              }
             }
-            if (v0) {
-              if (bad) flag_error(p.err, KVQ_DEV_ERR_RANGE);
-              if (!whole && half == 0) {
-                dst[128] = M;
-                dst[129] = l;
+            if (bad) flag_error(p.err, KVQ_DEV_ERR_RANGE);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (!whole && v0[r] && quad == 0) {
+                dst[r][128] = M[r];
+                dst[r][129] = l[r];
               }
-            }
           }
         }
         if (done) break;
-        M = -INFINITY;
-        l = zs = asc = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          M[r] = -INFINITY;
+          l[r] = zs[r] = asc[r] = 0.0f;
+          cl[r] = ncl[r];
+        }
         run = 0;
         k0 = wk.k;
       }
       const int buf = it & 1, v3 = it % 3;
-      const uint32_t tS = tm + uint32_t(buf) * kColS, tR = tc::lane_addr(tS, warp, 64 * half);
+      const uint32_t tS = tm + uint32_t(buf) * kColS + at;
       const bool raw = wk.raw();
       wait(sh, &sh.s_full[buf], uint32_t(it >> 1) & 1u, p.err);
       if (it >= 2) wait_pv(it - 2);
       __syncwarp();
       tc::fence_after();
       if (some) {
-        // first pass: the largest logit of this half (S is read again for the second)
-        float zb0 = 0.0f, zb1 = 0.0f, m0, m1;
-        uint32_t see0 = kFull, see1 = kFull;
-        if (!raw) {
-          uint32_t zr[2];
-          tc::ld<2>(tc::lane_addr(tS, warp, 128 + 2 * half), zr);
-          const int ng = (wk.s.np - wk.k * PPT) * (p.P / 32) - 2 * half;  // groups of this half that hold tokens (2 or more: all)
-          see0 = ng > 0 ? kFull : 0u;
-          see1 = ng > 1 ? kFull : 0u;
-          m0 = largest<false>(tR, kFull);
-          m1 = largest<false>(tR + 32, kFull);
-          asm volatile("" : "+r"(zr[0]), "+r"(zr[1]));
-          zb0 = __uint_as_float(zr[0]) * cl;
-          zb1 = __uint_as_float(zr[1]) * cl;
-        } else {
-          // bit j of see0, see1: the row sees token j, 32 + j of its half
-          const int x0 = 128 * (wk.k - wk.s.ntp) + 64 * half;
-          auto sees = [&](int xw) {
-            const int in_window = u_rl - xw, d = xw - u_rl;  // d: first drafted token of the word
-            uint32_t v = in_window >= 32 ? kFull : in_window > 0 ? (1u << in_window) - 1u : 0u;
-            if (d > -32) {
-              const int wd = d >> 5;
-              uint32_t a = 0u, b = 0u;
+        const int ng = raw ? 4 : min(4, (wk.s.np - wk.k * PPT) * (p.P / 32));  // groups of the tile that hold tokens
+        uint32_t zr[2] = {0u, 0u};  // q . z of group `quad`
+        if (!raw) ld4(tS + 128, zr);
+        // bits of the tokens the row sees among 32 from token x of the raw sequence on, the lane's first lowest
+        auto sees = [&](int xw, uint32_t (&see)[2]) {
+          const int in_window = u_rl - xw, d = xw - u_rl, wd = d >> 5;  // d: first drafted token of the word
+          const uint32_t v = in_window >= 32 ? kFull : in_window > 0 ? (1u << in_window) - 1u : 0u;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                a = j == wd ? mk[j] : a;
-                b = j == wd + 1 ? mk[j] : b;
-              }
-              v |= __funnelshift_r(a, b, uint32_t(d) & 31u);
-            }
-            return v;
-          };
-          see0 = sees(x0);
-          see1 = sees(x0 + 32);
-          m0 = largest<true>(tR, see0);
-          m1 = largest<true>(tR + 32, see1);
+          for (int r = 0; r < 2; ++r) {
+            const uint4 mk = r ? mk1 : mk0;
+            const uint32_t a = wd == 0 ? mk.x : wd == 1 ? mk.y : wd == 2 ? mk.z : wd == 3 ? mk.w : 0u;
+            const uint32_t b = wd == -1 ? mk.x : wd == 0 ? mk.y : wd == 1 ? mk.z : wd == 2 ? mk.w : 0u;
+            see[r] = (v | (d > -32 ? __funnelshift_r(a, b, uint32_t(d) & 31u) : 0u)) >> (2 * quad);
+          }
+        };
+        const int x0 = 128 * (wk.k - wk.s.ntp);
+        // first pass: the rows' largest logits (S is read again for the second)
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int g = 0; g < ng; ++g) {
+          float m[2];
+          uint32_t see[2] = {1u, 1u};
+          if (!raw) {
+            largest<false>(tS + 32 * g, see, m);
+          } else {
+            sees(x0 + 32 * g, see);
+            largest<true>(tS + 32 * g, see, m);
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float z = __shfl_sync(kFull, __uint_as_float(zr[r]), (lane & ~3) + g);
+            if (m[r] != -INFINITY) mx[r] = fmaxf(mx[r], (m[r] + z) * cl[r]);
+          }
         }
-        float mx = fmaxf(see0 ? fmaf(m0, cl, zb0) : -INFINITY, see1 ? fmaf(m1, cl, zb1) : -INFINITY);
-        sh.xch[buf][row][half] = mx;
-        pair_sync(1 + quarter);
-        mx = fmaxf(mx, sh.xch[buf][row][half ^ 1]);
         float sm;
         if (!raw) {
           sm = fmaxf(fmaxf(sh.smax[v3][0], sh.smax[v3][1]), fmaxf(sh.smax[v3][2], sh.smax[v3][3]));
@@ -1009,47 +1026,68 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         // sm < 2^lg; probabilities are carried as 2^(x - M + 7), so p * s starts below 2^7
         const float lg = float(max(-20, int((__float_as_uint(sm) >> 23) & 0xff) - 126));
-        mx += lg;
-        float alpha = 1.0f;
-        if (mx > M + 8.0f) {  // p * s could pass 2^15
-          alpha = ex2(M - mx);  // M = -inf: 0
-          l *= alpha;
-          zs *= alpha;
-          asc *= alpha;
-          M = mx;
+        float alpha[2], nm[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float top = quad_max(mx[r]) + lg;
+          alpha[r] = 1.0f;
+          if (top > M[r] + 8.0f) {  // p * s could pass 2^15
+            alpha[r] = ex2(M[r] - top);  // M = -inf: 0
+            l[r] *= alpha[r];
+            zs[r] *= alpha[r];
+            asc[r] *= alpha[r];
+            M[r] = top;
+          }
+          nm[r] = M[r] == -INFINITY ? 0.0f : 7.0f - M[r];
+        }
+        // second pass; a group without tokens holds old sums, which may be no number
+        const float4* sz = &sh.sz[v3][quad];
+        float tl[2] = {0.0f, 0.0f}, tz[2] = {0.0f, 0.0f};
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          uint32_t see[2] = {0u, 0u};
+          float off[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            off[r] = fmaf(__shfl_sync(kFull, __uint_as_float(zr[r]), (lane & ~3) + g), cl[r], nm[r]);
+          if (!raw && g < ng) {
+            weights<false>(tS + 32 * g, cl, off, see, sz + 16 * g, tl, tz);
+          } else {
+            if (raw) sees(x0 + 32 * g, see);
+            weights<true>(tS + 32 * g, cl, off, see, sz + 16 * g, tl, tz);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          l[r] += tl[r];
+          zs[r] += tz[r];
         }
         const bool flush = run > 0 && run % kFlush == 0;
-        if (flush || (run > 0 && __any_sync(kFull, alpha != 1.0f))) {
+        if (flush || (run > 0 && __any_sync(kFull, alpha[0] != 1.0f || alpha[1] != 1.0f))) {
           // O into the sums, to start anew with this tile; or only to the new reference
           wait_pv(it - 1);
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             uint32_t o[16];
-            tc::ld<16>(tO + 16 * i, o);
-            wait_ld(o);
+            ld32(tm + kColO + at + 32 * i, o);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[(j >> 1) & 1]);
             if (flush) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float4& a = acc[(4 * i + j) * 128];
-                const float4 x = asc != 0.0f ? a : make_float4(0.f, 0.f, 0.f, 0.f);
-                a = make_float4(fmaf(x.x, asc, __uint_as_float(o[4 * j])), fmaf(x.y, asc, __uint_as_float(o[4 * j + 1])),
-                                fmaf(x.z, asc, __uint_as_float(o[4 * j + 2])), fmaf(x.w, asc, __uint_as_float(o[4 * j + 3])));
-              }
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  float2& a = sums(16 * i + 4 * c + quad, r);
+                  const float2 x = asc[r] != 0.0f ? a : make_float2(0.f, 0.f);
+                  a = make_float2(fmaf(x.x, asc[r], __uint_as_float(o[4 * c + 2 * r])),
+                                  fmaf(x.y, asc[r], __uint_as_float(o[4 * c + 2 * r + 1])));
+                }
             } else {
-              tc::st<16>(tO + 16 * i, o);
+              st32(tm + kColO + at + 32 * i, o);
             }
           }
-          if (flush) asc = 1.0f;
+          if (flush) asc[0] = asc[1] = 1.0f;
         }
-        // second pass; a group without tokens holds old sums, which may be no number
-        const float nm = M == -INFINITY ? 0.0f : 7.0f - M;
-        const float *vs = &sh.vs[v3][64 * half], *vz = &sh.vz[v3][64 * half];
-        if (raw || see1 == 0u)
-          weights<true>(tR, cl, zb0 + nm, zb1 + nm, see0, see1, vs, vz, l, zs);
-        else
-          weights<false>(tR, cl, zb0 + nm, zb1 + nm, kFull, kFull, vs, vz, l, zs);
         tc::wait_st();
       }
       tc::fence_before();
