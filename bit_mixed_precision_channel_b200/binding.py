@@ -96,6 +96,15 @@ class Config:
                        self.key_group, self.key_bits, self.boost_bits, self.value_bits,
                        self.num_boost, self.dtype)
 
+    def _marshalled(self):
+        """(pointer to the C structure, torch dtype, bytes of one page of all KV heads), made once:
+        a serving step makes the same call for every layer."""
+        m = self.__dict__.get("_m")
+        if m is None:
+            m = (ctypes.byref(self.c()), torch_dtype(self.dtype), self.num_kv_heads * page_bytes(self))
+            object.__setattr__(self, "_m", m)
+        return m
+
 
 def torch_dtype(dtype: int) -> torch.dtype:
     return torch.bfloat16 if dtype == BF16 else torch.float16
@@ -199,7 +208,13 @@ def load():
     return _lib
 
 
+# the current stream's handle without a Stream object around it (3 us less a call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
 
@@ -252,6 +267,21 @@ def _need(name: str, t, dtype=None, numel: int | None = None, dim: int | None = 
         raise ValueError(f"{name}: {t.numel()} elements, the call reads {numel}")
 
 
+def _vet(stream, *specs) -> int:
+    """_need and _cuda over (name, tensor, element type, least elements) in one pass, for the
+    calls of a decode step; returns the stream."""
+    dev = cur = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    for name, t, dtype, numel in specs:
+        if t is not None:
+            if t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel:
+                _need(name, t, dtype, numel)
+            if t.get_device() != cur:
+                dev = -1
+    if dev < 0 or stream is not None:
+        _cuda(*(t for _, t, _, _ in specs), stream=stream)
+    return _stream(stream)
+
+
 def _need_source(name: str, src, cfg: Config, n_pages: int):
     if src is None:
         return
@@ -278,10 +308,6 @@ def page_layout(cfg: Config) -> dict:
 
 def page_bytes(cfg: Config) -> int:
     return int(load().kvq_page_bytes(ctypes.byref(cfg.c())))
-
-
-def _pool_pages(cfg: Config, pool: torch.Tensor) -> int:
-    return pool.numel() // (cfg.num_kv_heads * page_bytes(cfg))
 
 
 def _boost_options(cfg: Config, query_weight, boost_per_head):
@@ -467,47 +493,50 @@ def decode_attention_static(cfg: Config, pool, q, page_table, num_pages, res_k, 
         float(sm_scale), out.data_ptr(), _ptr(err), _stream(stream)))
 
 
+def _need_slots(cfg: Config, sel, batch: int):
+    _need("sel", sel, torch.int32, dim=3)
+    if sel.shape[0] != batch or sel.shape[1] != cfg.num_kv_heads:
+        raise ValueError(f"sel: shape {tuple(sel.shape)}, the call takes [{batch}][{cfg.num_kv_heads}][slots]")
+
+
 def select_pages(cfg: Config, pool, q, page_table, num_pages, sel, n_sel, n_first: int = 0, n_recent: int = 0,
                  err=None, stream=None):
     """Chooses the pages a decode step reads: sel int32 [B][Hkv][n_select] receives the slots
     of the page table with the largest logit bounds (the first n_first and the last n_recent
     pages always), ascending, then -1; n_sel int32 [B] their number."""
-    _need("page_table", page_table, torch.int32, dim=2)
+    c, dt, page = cfg._marshalled()
+    i32 = torch.int32
+    _need("page_table", page_table, i32, dim=2)
     batch, max_pages = page_table.shape
-    _need("sel", sel, torch.int32, dim=3)
-    if sel.shape[0] != batch or sel.shape[1] != cfg.num_kv_heads:
-        raise ValueError(f"sel: shape {tuple(sel.shape)}, the call writes [{batch}][{cfg.num_kv_heads}][n_select]")
-    _need("pool", pool, torch.uint8)
-    _need("q", q, torch_dtype(cfg.dtype), batch * cfg.num_q_heads * cfg.head_dim)
-    _need("num_pages", num_pages, torch.int32, batch)
-    _need("n_sel", n_sel, torch.int32, batch)
-    _need("err", err, torch.int32, 1)
-    _cuda(pool, q, page_table, num_pages, sel, n_sel, err, stream=stream)
+    _need_slots(cfg, sel, batch)
+    st = _vet(stream, ("pool", pool, torch.uint8, 0), ("q", q, dt, batch * cfg.num_q_heads * cfg.head_dim),
+              ("page_table", page_table, i32, 0), ("num_pages", num_pages, i32, batch), ("sel", sel, i32, 0),
+              ("n_sel", n_sel, i32, batch), ("err", err, i32, 1))
     _check("kvq_select_pages", load().kvq_select_pages(
-        ctypes.byref(cfg.c()), pool.data_ptr(), _pool_pages(cfg, pool), q.data_ptr(), batch, page_table.data_ptr(),
-        max_pages, num_pages.data_ptr(), n_first, n_recent, sel.shape[2], sel.data_ptr(), n_sel.data_ptr(), _ptr(err),
-        _stream(stream)))
+        c, pool.data_ptr(), pool.numel() // page, q.data_ptr(), batch, page_table.data_ptr(), max_pages,
+        num_pages.data_ptr(), n_first, n_recent, sel.shape[2], sel.data_ptr(), n_sel.data_ptr(), _ptr(err), st))
 
 
 def decode_attention_sparse(cfg: Config, pool, q, page_table, num_pages, sel, n_sel, res_k, res_v, res_len, out,
                             workspace, sm_scale: float | None = None, err=None, stream=None):
     """decode_attention over the pages in slots sel[b][kv head][:n_sel[b]] of the page table
     (sel int32 [B][Hkv][max_sel]) and the residual window."""
-    _need_decode(cfg, pool, q, page_table, num_pages, res_k, res_v, res_len, out, err)
+    c, dt, page = cfg._marshalled()
+    i32, D = torch.int32, cfg.head_dim
+    _need("page_table", page_table, i32, dim=2)
     batch, max_pages = page_table.shape
-    _need("sel", sel, torch.int32, dim=3)
-    if sel.shape[0] != batch or sel.shape[1] != cfg.num_kv_heads:
-        raise ValueError(f"sel: shape {tuple(sel.shape)}, the call reads [{batch}][{cfg.num_kv_heads}][max_sel]")
-    _need("n_sel", n_sel, torch.int32, batch)
-    _need("workspace", workspace, torch.uint8)
-    _cuda(pool, q, page_table, num_pages, sel, n_sel, res_k, res_v, res_len, out, workspace, err, stream=stream)
+    _need_slots(cfg, sel, batch)
+    rows, window = batch * cfg.num_q_heads * D, batch * cfg.num_kv_heads * cfg.page_tokens * D
+    st = _vet(stream, ("pool", pool, torch.uint8, 0), ("q", q, dt, rows), ("page_table", page_table, i32, 0),
+              ("num_pages", num_pages, i32, batch), ("sel", sel, i32, 0), ("n_sel", n_sel, i32, batch),
+              ("res_k", res_k, dt, window), ("res_v", res_v, dt, window), ("res_len", res_len, i32, batch),
+              ("out", out, torch.float32, rows), ("workspace", workspace, torch.uint8, 0), ("err", err, i32, 1))
     if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(cfg.head_dim)
+        sm_scale = 1.0 / math.sqrt(D)
     _check("kvq_decode_attention_sparse", load().kvq_decode_attention_sparse(
-        ctypes.byref(cfg.c()), pool.data_ptr(), _pool_pages(cfg, pool), q.data_ptr(), batch, page_table.data_ptr(),
-        max_pages, num_pages.data_ptr(), sel.data_ptr(), sel.shape[2], n_sel.data_ptr(), res_k.data_ptr(),
-        res_v.data_ptr(), res_len.data_ptr(), float(sm_scale), out.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), _ptr(err), _stream(stream)))
+        c, pool.data_ptr(), pool.numel() // page, q.data_ptr(), batch, page_table.data_ptr(), max_pages,
+        num_pages.data_ptr(), sel.data_ptr(), sel.shape[2], n_sel.data_ptr(), res_k.data_ptr(), res_v.data_ptr(),
+        res_len.data_ptr(), float(sm_scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(err), st))
 
 
 def tree_workspace_bytes(cfg: Config, batch: int, n_draft: int) -> int:
@@ -520,52 +549,42 @@ def tree_attention(cfg: Config, pool, q, page_table, num_pages, res_k, res_v, re
     mask names: q [B][T][Hq][D], k_draft and v_draft [B][T][Hkv][D] of the cache dtype, mask
     int32 [B][T][ceil(T/32)] (bit j % 32 of word j // 32), draft_len int32 [B], out fp32
     [B][T][Hq][D] (rows at or past draft_len[b] are left as they were)."""
-    dt, H, P, D = torch_dtype(cfg.dtype), cfg.num_kv_heads, cfg.page_tokens, cfg.head_dim
-    _need("page_table", page_table, torch.int32, dim=2)
+    c, dt, page = cfg._marshalled()
+    i32, D = torch.int32, cfg.head_dim
+    _need("page_table", page_table, i32, dim=2)
     batch, max_pages = page_table.shape
     _need("q", q, dt, dim=4)
     T = q.shape[1]
-    _need("q", q, dt, batch * T * cfg.num_q_heads * D)
-    _need("k_draft", k_draft, dt, batch * T * H * D)
-    _need("v_draft", v_draft, dt, batch * T * H * D)
-    _need("mask", mask, torch.int32, batch * T * ((T + 31) // 32))
-    _need("draft_len", draft_len, torch.int32, batch)
-    _need("out", out, torch.float32, batch * T * cfg.num_q_heads * D)
-    _need("pool", pool, torch.uint8)
-    _need("num_pages", num_pages, torch.int32, batch)
-    _need("res_len", res_len, torch.int32, batch)
-    _need("res_k", res_k, dt, batch * H * P * D)
-    _need("res_v", res_v, dt, batch * H * P * D)
-    _need("workspace", workspace, torch.uint8)
-    _need("err", err, torch.int32, 1)
-    _cuda(pool, q, page_table, num_pages, res_k, res_v, res_len, k_draft, v_draft, mask, draft_len, out, workspace,
-          err, stream=stream)
+    rows, kv = batch * T * cfg.num_q_heads * D, batch * T * cfg.num_kv_heads * D
+    window = batch * cfg.num_kv_heads * cfg.page_tokens * D
+    st = _vet(stream, ("q", q, dt, rows), ("k_draft", k_draft, dt, kv), ("v_draft", v_draft, dt, kv),
+              ("mask", mask, i32, batch * T * ((T + 31) // 32)), ("draft_len", draft_len, i32, batch),
+              ("out", out, torch.float32, rows), ("pool", pool, torch.uint8, 0), ("page_table", page_table, i32, 0),
+              ("num_pages", num_pages, i32, batch), ("res_len", res_len, i32, batch), ("res_k", res_k, dt, window),
+              ("res_v", res_v, dt, window), ("workspace", workspace, torch.uint8, 0), ("err", err, i32, 1))
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(D)
     _check("kvq_tree_attention", load().kvq_tree_attention(
-        ctypes.byref(cfg.c()), pool.data_ptr(), _pool_pages(cfg, pool), q.data_ptr(), T, batch, page_table.data_ptr(),
-        max_pages, num_pages.data_ptr(), res_k.data_ptr(), res_v.data_ptr(), res_len.data_ptr(), k_draft.data_ptr(),
+        c, pool.data_ptr(), pool.numel() // page, q.data_ptr(), T, batch, page_table.data_ptr(), max_pages,
+        num_pages.data_ptr(), res_k.data_ptr(), res_v.data_ptr(), res_len.data_ptr(), k_draft.data_ptr(),
         v_draft.data_ptr(), mask.data_ptr(), draft_len.data_ptr(), float(sm_scale), out.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), _ptr(err), _stream(stream)))
+        workspace.data_ptr(), workspace.numel(), _ptr(err), st))
 
 
 def append_path(cfg: Config, k_draft, v_draft, path, n_path, taken, res_k, res_v, res_len, err=None, stream=None):
     """Tokens path[b][taken[b]:n_path[b]] of k_draft and v_draft [B][T][Hkv][D] behind the
     residual window, as many as fit; res_len and taken (int32 [B]) advance by that number."""
-    dt, H, P, D = torch_dtype(cfg.dtype), cfg.num_kv_heads, cfg.page_tokens, cfg.head_dim
-    _need("path", path, torch.int32, dim=2)
+    c, dt, _ = cfg._marshalled()
+    i32, D = torch.int32, cfg.head_dim
+    _need("path", path, i32, dim=2)
     batch, T = path.shape
-    _need("k_draft", k_draft, dt, batch * T * H * D)
-    _need("v_draft", v_draft, dt, batch * T * H * D)
-    for name, t in (("n_path", n_path), ("taken", taken), ("res_len", res_len)):
-        _need(name, t, torch.int32, batch)
-    _need("res_k", res_k, dt, batch * H * P * D)
-    _need("res_v", res_v, dt, batch * H * P * D)
-    _need("err", err, torch.int32, 1)
-    _cuda(k_draft, v_draft, path, n_path, taken, res_k, res_v, res_len, err, stream=stream)
+    kv, window = batch * T * cfg.num_kv_heads * D, batch * cfg.num_kv_heads * cfg.page_tokens * D
+    st = _vet(stream, ("k_draft", k_draft, dt, kv), ("v_draft", v_draft, dt, kv), ("path", path, i32, 0),
+              ("n_path", n_path, i32, batch), ("taken", taken, i32, batch), ("res_len", res_len, i32, batch),
+              ("res_k", res_k, dt, window), ("res_v", res_v, dt, window), ("err", err, i32, 1))
     _check("kvq_append_path", load().kvq_append_path(
-        ctypes.byref(cfg.c()), batch, T, k_draft.data_ptr(), v_draft.data_ptr(), path.data_ptr(), n_path.data_ptr(),
-        taken.data_ptr(), res_k.data_ptr(), res_v.data_ptr(), res_len.data_ptr(), _ptr(err), _stream(stream)))
+        c, batch, T, k_draft.data_ptr(), v_draft.data_ptr(), path.data_ptr(), n_path.data_ptr(), taken.data_ptr(),
+        res_k.data_ptr(), res_v.data_ptr(), res_len.data_ptr(), _ptr(err), st))
 
 
 def dense_page_bytes(cfg: Config) -> int:
