@@ -217,7 +217,7 @@ struct Line {
 template <int NT>
 __device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta, int ctas, bool flag) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int total = 0;
+  int total = 0, x = 0, incl = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     int run = 0, at = 0;
@@ -232,20 +232,22 @@ __device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta
 #pragma unroll 1
     for (int base = 0; base < p.batch; base += NT) {
       const int b = base + tid;
-      int x = 0;
-      if (b < p.batch) {
-        Seq s;
-        if (!seq_load(p, b, s) && flag && pass == 0) flag_error(p.err, KVQ_DEV_ERR_LENGTH);
-        x = seq_tiles(p, s);
-      }
-      int incl = x;
+      if (pass == 0 || p.batch > NT) {  // (with a sequence a thread its tiles and their sums stay)
+        x = 0;
+        if (b < p.batch) {
+          Seq s;
+          if (!seq_load(p, b, s) && flag && pass == 0) flag_error(p.err, KVQ_DEV_ERR_LENGTH);
+          x = seq_tiles(p, s);
+        }
+        incl = x;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(kFull, incl, off);
-        if (lane >= off) incl += y;
+        for (int off = 1; off < 32; off <<= 1) {
+          const int y = __shfl_up_sync(kFull, incl, off);
+          if (lane >= off) incl += y;
+        }
+        if (lane == 31) ln.sums[warp] = incl;
+        __syncthreads();
       }
-      if (lane == 31) ln.sums[warp] = incl;
-      __syncthreads();
       int before = run, all = 0;
 #pragma unroll 4
       for (int w = 0; w < NT / 32; ++w) {
@@ -257,7 +259,7 @@ __device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta
         ln.b0 = b;
         ln.base0 = before + incl - x;
       }
-      __syncthreads();
+      if (p.batch > NT) __syncthreads();
     }
     total = run;
   }
@@ -353,6 +355,9 @@ __device__ __forceinline__ void list_moves(const uint8_t* idx, Moves& mv, int la
 }
 
 // Keys of token `row` of the tile (token tp of the page record): the 32 channels of (half, a).
+// The operands' contraction axis has its own order of channels, the one in which the record
+// keeps scales and zero points: 16 bytes number 4 cc + q of a row are the pairs q of the four
+// groups of 8 channels 4 cc .. 4 cc + 3 (cc = 2 half + a).
 template <typename T, int KB>
 __device__ __forceinline__ void key_row(const TreeParams& p, const uint8_t* rec, int tp, int row, int half, int a,
                                         uint8_t* smem, const Moves& mv) {
@@ -397,11 +402,11 @@ __device__ __forceinline__ void key_row(const TreeParams& p, const uint8_t* rec,
       wb[2 * qp + 1] = acc >> 2;
     }
   }
-  uint32_t hi[4][4], lo[4][4];  // [q][i]
   const uint8_t* sc = rec + p.L.k_scale + (tp >> 5) * 256 + 64 * (2 * half + a);
+  uint8_t* dst = smem + tco(row, 4 * (2 * half + a));
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    uint32_t u[4];
+    uint32_t u[4], lo[4];
     e2m1_pairs(code_pass(w[q], a), u[0], u[1], u[2], u[3]);
     if constexpr (KB > 0) {
       uint32_t ub[4];
@@ -415,15 +420,11 @@ __device__ __forceinline__ void key_row(const TreeParams& p, const uint8_t* rec,
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __half2 x = __hmul2(u32_as_h2(u[i]), u32_as_h2(s[i]));
-      hi[q][i] = h2_as_u32(x);
-      lo[q][i] = h2_as_u32(__hfma2(u32_as_h2(u[i]), u32_as_h2(s[i]), __hneg2(x)));
+      lo[i] = h2_as_u32(__hfma2(u32_as_h2(u[i]), u32_as_h2(s[i]), __hneg2(x)));
+      u[i] = h2_as_u32(x);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t at = tco(row, 8 * half + 4 * a + i);
-    *reinterpret_cast<uint4*>(smem + kKhi + at) = make_uint4(hi[0][i], hi[1][i], hi[2][i], hi[3][i]);
-    *reinterpret_cast<uint4*>(smem + kKlo + at) = make_uint4(lo[0][i], lo[1][i], lo[2][i], lo[3][i]);
+    *reinterpret_cast<uint4*>(dst + kKhi + 128 * q) = make_uint4(u[0], u[1], u[2], u[3]);
+    *reinterpret_cast<uint4*>(dst + kKlo + 128 * q) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
@@ -470,13 +471,12 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x, uint32_t expo, bool& bad
 
 // ---------------------------------------------------------------- softmax
 
-// 32 logits of the lane's two rows at columns tR .. tR + 31, as 2^(cl S + off), 0 where the
-// token's bit of see is clear (MASK), times the tokens' value scales, back in the same columns
-// as fp16 high and low parts: every 16 tokens in 8 + 8 columns.  sz: {s, s', z, z'} of the
-// tokens' pairs, from the lane's first on.  The sums (also with z) go to l and zs.
-template <bool MASK>
-__device__ __forceinline__ void weights(uint32_t tR, const float (&cl)[2], const float (&off)[2], const uint32_t (&see)[2],
-                                        const float4* sz, float (&l)[2], float (&zs)[2]) {
+// 32 logits of the lane's two rows at columns tR .. tR + 31, as 2^(cl S + off), times the
+// tokens' value scales, back in the same columns as fp16 high and low parts: every 16 tokens
+// in 8 + 8 columns.  sz: {s, s', z, z'} of the tokens' pairs, from the lane's first on.  The
+// sums (also with z) go to l and zs.
+__device__ __forceinline__ void weights(uint32_t tR, const float (&cl)[2], const float (&off)[2], const float4* sz,
+                                        float (&l)[2], float (&zs)[2]) {
   uint32_t x[16];
   ld32(tR, x);
 #pragma unroll
@@ -489,10 +489,6 @@ __device__ __forceinline__ void weights(uint32_t tR, const float (&cl)[2], const
       for (int r = 0; r < 2; ++r) {
         float p0 = ex2(__fmaf_rn(__uint_as_float(x[4 * (c + d) + 2 * r]), cl[r], off[r]));
         float p1 = ex2(__fmaf_rn(__uint_as_float(x[4 * (c + d) + 2 * r + 1]), cl[r], off[r]));
-        if (MASK) {  // see is shifted to the lane's first token
-          p0 = (see[r] >> (8 * (c + d))) & 1u ? p0 : 0.0f;
-          p1 = (see[r] >> (8 * (c + d) + 1)) & 1u ? p1 : 0.0f;
-        }
         l[r] += p0 + p1;
         zs[r] = fmaf(p0, v.z, zs[r]);
         zs[r] = fmaf(p1, v.w, zs[r]);
@@ -506,24 +502,6 @@ __device__ __forceinline__ void weights(uint32_t tR, const float (&cl)[2], const
     }
     st8(tR + 8 * c, hi[0][0], hi[0][1], hi[1][0], hi[1][1]);
     st8(tR + 8 * c + 8, lo[0][0], lo[0][1], lo[1][0], lo[1][1]);
-  }
-}
-
-// The largest of the lane's logits S among 32 columns whose bit of see is set (MASK), -inf if
-// there is none; masked values may be no number.
-template <bool MASK>
-__device__ __forceinline__ void largest(uint32_t tR, const uint32_t (&see)[2], float (&m)[2]) {
-  uint32_t x[16];
-  ld32(tR, x);
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      a = fmaxf(a, !MASK || ((see[r] >> (8 * c)) & 1u) ? __uint_as_float(x[4 * c + 2 * r]) : -INFINITY);
-      b = fmaxf(b, !MASK || ((see[r] >> (8 * c + 1)) & 1u) ? __uint_as_float(x[4 * c + 2 * r + 1]) : -INFINITY);
-    }
-    m[r] = fmaxf(a, b);
   }
 }
 
@@ -731,12 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             key_row<T, KB>(p, rec, 32 * gp + lane, 32 * g + lane, half, a, smem, sh.moves[kMoves ? st : 0][kMoves ? pg : 0]);
         if (half == 0) {
           if (have && lane < 16) {  // zero points: row 128 + g of the key operand
-            const int s = lane >> 1, r = lane & 1;
-            const uint8_t* z = rec + p.L.k_zero + gp * 256 + (32 * (s >> 1) + 4 * (s & 1) + 2 * r) * 2;
-            uint32_t x[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) x[q] = half_of(meta_h2(lds32(z + 16 * q), T()));
-            *reinterpret_cast<uint4*>(smem + kKhi + tco(128 + g, lane)) = make_uint4(x[0], x[1], x[2], x[3]);
+            const uint4 z = lds128(rec + p.L.k_zero + gp * 256 + 16 * lane);
+            *reinterpret_cast<uint4*>(smem + kKhi + tco(128 + g, lane)) =
+                make_uint4(half_of(meta_h2(z.x, T())), half_of(meta_h2(z.y, T())), half_of(meta_h2(z.z, T())),
+                           half_of(meta_h2(z.w, T())));
           }
         } else {
           float s = 0.0f, z = 0.0f;
@@ -785,7 +761,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const float2 y = unpack2(finite2(v[e], BF ? 0x7f80u : 0x7c00u, bad), T());
             m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
           }
-          *reinterpret_cast<uint4*>(smem + kKhi + tco(t, c)) = make_uint4(k[0], k[1], k[2], k[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)  // pair e of 8 channels c: the operand's order
+            *reinterpret_cast<uint32_t*>(smem + kKhi + tco(t, (c & ~3) + e) + 4 * (c & 3)) = k[e];
           if (bad && (!draft || seen_by_any(p, wk.b, wk.s.dl, x - wk.s.rl))) flag_error(p.err, KVQ_DEV_ERR_RANGE);
           float s = 0.5f;
           if constexpr (BF) {  // the power of two below the token's largest value
@@ -885,16 +863,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           u_dl = wk.s.dl;
           u_rl = wk.s.rl;
           if (some) {
-            uint32_t v[32];  // [8 channels][row]: channels 2 quad, 2 quad + 1
+            uint32_t v[2][16];  // [row][cc][pair]: channels 8 (4 cc + quad) + 2 pair, the operand's order
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const int R = 128 * wk.r + row + 8 * r, i = R / p.gqa;
               valid[r] = i < wk.s.dl;
               orow[r] = (size_t(wk.b) * p.T + i) * p.Hq + wk.h * p.gqa + (R - i * p.gqa);
-              const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + orow[r] * kHeadDim) + quad;
+              const uint4* src = reinterpret_cast<const uint4*>(p.q + orow[r] * kHeadDim) + quad;
               float m = 0.0f;
 #pragma unroll
-              for (int c = 0; c < 16; ++c) v[2 * c + r] = valid[r] ? __ldcg(src + 4 * c) : 0u;
+              for (int c = 0; c < 4; ++c) {
+                const uint4 x = valid[r] ? __ldcg(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
+                v[r][4 * c] = x.x;
+                v[r][4 * c + 1] = x.y;
+                v[r][4 * c + 2] = x.z;
+                v[r][4 * c + 3] = x.w;
+              }
               auto mask = [&](int j) {
                 const int left = u_dl - 32 * j;
                 return valid[r] && left > 0 ? __ldcg(p.mask + (size_t(wk.b) * p.T + i) * p.W + j) &
@@ -904,23 +888,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               (r ? mk1 : mk0) = make_uint4(mask(0), mask(1), mask(2), mask(3));
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
-                const float2 f = unpack2(v[2 * c + r], T());
+                const float2 f = unpack2(v[r][c], T());
                 m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
               }
               m = quad_max(m);
               // |q| < 2^e; e = 0 below 1
               const int e = min(max(int((__float_as_uint(m) >> 23) & 0xff) - 126, 0), 126);
               const float f = p.c_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
-              ncl[r] = 2.0f * fabsf(p.c_log2) * pow2i(e);
+              ncl[r] = fmaxf(2.0f * fabsf(p.c_log2) * pow2i(e), 1e-30f);  // above 0: a masked -inf stays one
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
-                const float2 y = unpack2(v[2 * c + r], T());
-                v[2 * c + r] = pack_h2(y.x * f, y.y * f);
+                const float2 y = unpack2(v[r][c], T());
+                v[r][c] = pack_h2(y.x * f, y.y * f);
               }
             }
 #pragma unroll
-            for (int c = 0; c < 16; c += 2)
-              st8(tm + kColQ + at + 4 * c, v[2 * c], v[2 * c + 1], v[2 * c + 2], v[2 * c + 3]);
+            for (int c = 0; c < 16; c += 2) st8(tm + kColQ + at + 4 * c, v[0][c], v[1][c], v[0][c + 1], v[1][c + 1]);
             tc::wait_st();
           }
           tc::fence_before();
@@ -982,38 +965,49 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       __syncwarp();
       tc::fence_after();
       if (some) {
-        const int ng = raw ? 4 : min(4, (wk.s.np - wk.k * PPT) * (p.P / 32));  // groups of the tile that hold tokens
         uint32_t zr[2] = {0u, 0u};  // q . z of group `quad`
         if (!raw) ld4(tS + 128, zr);
-        // bits of the tokens the row sees among 32 from token x of the raw sequence on, the lane's first lowest
-        auto sees = [&](int xw, uint32_t (&see)[2]) {
-          const int in_window = u_rl - xw, d = xw - u_rl, wd = d >> 5;  // d: first drafted token of the word
-          const uint32_t v = in_window >= 32 ? kFull : in_window > 0 ? (1u << in_window) - 1u : 0u;
+        if (raw || wk.s.np - wk.k * PPT < PPT) {
+          // masked places, whatever they hold, become -inf: tokens that are not there or not seen
+          const int ng = raw ? 0 : (wk.s.np - wk.k * PPT) * (p.P / 32);  // groups that hold tokens
+          if (quad >= ng) zr[0] = zr[1] = 0u;
+#pragma unroll 1
+          for (int g = ng; g < 4; ++g) {
+            uint32_t x[16], see[2] = {0u, 0u};
+            ld32(tS + 32 * g, x);
+            if (raw) {
+              // bits of the 32 tokens from token xw of the raw sequence on, the lane's first lowest
+              const int xw = 128 * (wk.k - wk.s.ntp) + 32 * g, in_window = u_rl - xw;
+              const int d = xw - u_rl, wd = d >> 5;  // d: first drafted token of the word
+              const uint32_t v = in_window >= 32 ? kFull : in_window > 0 ? (1u << in_window) - 1u : 0u;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint4 mk = r ? mk1 : mk0;
-            const uint32_t a = wd == 0 ? mk.x : wd == 1 ? mk.y : wd == 2 ? mk.z : wd == 3 ? mk.w : 0u;
-            const uint32_t b = wd == -1 ? mk.x : wd == 0 ? mk.y : wd == 1 ? mk.z : wd == 2 ? mk.w : 0u;
-            see[r] = (v | (d > -32 ? __funnelshift_r(a, b, uint32_t(d) & 31u) : 0u)) >> (2 * quad);
+              for (int r = 0; r < 2; ++r) {
+                const uint4 mk = r ? mk1 : mk0;
+                const uint32_t m0 = wd == 0 ? mk.x : wd == 1 ? mk.y : wd == 2 ? mk.z : wd == 3 ? mk.w : 0u;
+                const uint32_t m1 = wd == -1 ? mk.x : wd == 0 ? mk.y : wd == 1 ? mk.z : wd == 2 ? mk.w : 0u;
+                see[r] = (v | (d > -32 ? __funnelshift_r(m0, m1, uint32_t(d) & 31u) : 0u)) >> (2 * quad);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (!((see[(j >> 1) & 1] >> (8 * (j >> 2) + (j & 1))) & 1u)) x[j] = 0xff800000u;
+            st32(tS + 32 * g, x);
           }
-        };
-        const int x0 = 128 * (wk.k - wk.s.ntp);
+          tc::wait_st();
+        }
         // first pass: the rows' largest logits (S is read again for the second)
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
-        for (int g = 0; g < ng; ++g) {
-          float m[2];
-          uint32_t see[2] = {1u, 1u};
-          if (!raw) {
-            largest<false>(tS + 32 * g, see, m);
-          } else {
-            sees(x0 + 32 * g, see);
-            largest<true>(tS + 32 * g, see, m);
-          }
+        for (int g = 0; g < 4; ++g) {
+          uint32_t x[16];
+          ld32(tS + 32 * g, x);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float z = __shfl_sync(kFull, __uint_as_float(zr[r]), (lane & ~3) + g);
-            if (m[r] != -INFINITY) mx[r] = fmaxf(mx[r], (m[r] + z) * cl[r]);
+            float m = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              m = fmaxf(m, fmaxf(__uint_as_float(x[4 * c + 2 * r]), __uint_as_float(x[4 * c + 2 * r + 1])));
+            mx[r] = fmaxf(mx[r], m + __shfl_sync(kFull, __uint_as_float(zr[r]), (lane & ~3) + g));
           }
         }
         float sm;
@@ -1029,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         float alpha[2], nm[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float top = quad_max(mx[r]) + lg;
+          const float top = fmaf(quad_max(mx[r]), cl[r], lg);
           alpha[r] = 1.0f;
           if (top > M[r] + 8.0f) {  // p * s could pass 2^15
             alpha[r] = ex2(M[r] - top);  // M = -inf: 0
@@ -1040,22 +1034,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
           nm[r] = M[r] == -INFINITY ? 0.0f : 7.0f - M[r];
         }
-        // second pass; a group without tokens holds old sums, which may be no number
+        // second pass
         const float4* sz = &sh.sz[v3][quad];
         float tl[2] = {0.0f, 0.0f}, tz[2] = {0.0f, 0.0f};
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {
-          uint32_t see[2] = {0u, 0u};
           float off[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r)
             off[r] = fmaf(__shfl_sync(kFull, __uint_as_float(zr[r]), (lane & ~3) + g), cl[r], nm[r]);
-          if (!raw && g < ng) {
-            weights<false>(tS + 32 * g, cl, off, see, sz + 16 * g, tl, tz);
-          } else {
-            if (raw) sees(x0 + 32 * g, see);
-            weights<true>(tS + 32 * g, cl, off, see, sz + 16 * g, tl, tz);
-          }
+          weights(tS + 32 * g, cl, off, sz + 16 * g, tl, tz);
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
