@@ -430,7 +430,8 @@ kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int64_t poo
 
 size_t kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n_draft) {
   if (kvq_check_config(cfg) != KVQ_OK || batch < 0 || n_draft < 1 || n_draft > KVQ_MAX_DRAFT) return 0;
-  return size_t(2) * sm_count() * 128 * (kHeadDim + 4) * sizeof(float);
+  // two parts of 128 rows and one list entry per CTA
+  return size_t(sm_count()) * (2 * 128 * (kHeadDim + 4) * sizeof(float) + sizeof(int4));
 }
 
 kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
@@ -480,6 +481,7 @@ kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t p
   p.out = out;
   p.part = static_cast<float*>(workspace);
   p.n_ctas = sm_count();
+  p.cuts = reinterpret_cast<int4*>(p.part + size_t(p.n_ctas) * 2 * 128 * (kHeadDim + 4));
   p.err = err;
   return cuda_status(launch_tree(p, cfg->dtype, stream));
 }

@@ -388,6 +388,7 @@ struct TreeParams {
   float c_log2;
   float* out;  // [batch][T][Hq][128]
   float* part;  // [2 * n_ctas][128][132]: rows of units cut by a range boundary
+  int4* cuts;   // [n_ctas]: the cut units, {sequence, kv head and row tile, first and last CTA} or -1
   int n_ctas;   // grid size: one CTA per SM
   int32_t* err;
 };

@@ -15,7 +15,7 @@
 // Per tile, with thread roles that run ahead of one another through mbarriers:
 //   producer   1 warp    copies the page records (one bulk copy each, three tiles ahead);
 //   mover      1 warp    lists where the boosted channels' plane-B codes go;
-//   dequant    8 warps   write the keys of a tile, then the value codes of the tile before,
+//   dequant   16 warps   write the keys of a tile, then the value codes of the tile before,
 //                        as fp16 operands;
 //   issuer     1 warp    S = Q K^T, then O += P V of the tile before (tcgen05, M = 128);
 //   softmax    8 warps   16 rows each, four lanes a row: S from tensor memory, running
@@ -48,14 +48,14 @@ namespace tree {
 
 // The code of all roles together has to stay in the instruction caches, so the roles' loops
 // are rolled (unrolled, 130 KB of code, the same work took XX us instead of YY).
-constexpr int kSoftWarps = 8, kDeqWarps = 8;
+constexpr int kSoftWarps = 8, kDeqWarps = 16;
 constexpr int kIssuer = kSoftWarps + kDeqWarps, kProducer = kIssuer + 1, kMover = kIssuer + 2;
-constexpr int kThreads = 640;  // 5 warpgroups: two of softmax, two of dequant, one of single warps
-// Registers a thread: at launch, then by role (setmaxnreg): 2 x 120 + 2 x 88 + 64 = 5 x 96,
+constexpr int kThreads = 896;  // 7 warpgroups: two of softmax, four of dequant, one of single warps
+// Registers a thread: at launch, then by role (setmaxnreg): 2 x 112 + 4 x 56 + 56 = 7 x 72,
 // so the split draws on exactly what the block was launched with.  The shared memory leaves
 // next to no L1, so a register spilled in a role's loop costs an L2 access.
-constexpr int kRegsLaunch = 96, kRegsSoft = 120, kRegsDeq = 88, kRegsRest = 64;
-static_assert(2 * kRegsSoft + 2 * kRegsDeq + kRegsRest <= 5 * kRegsLaunch, "register split");
+constexpr int kRegsLaunch = 72, kRegsSoft = 112, kRegsDeq = 56, kRegsRest = 56;
+static_assert(2 * kRegsSoft + 4 * kRegsDeq + kRegsRest <= 7 * kRegsLaunch, "register split");
 constexpr int kRecStages = 3;
 // The tensor cores round their fp32 accumulator toward zero: 16 products a tile shrink a long
 // sum by about 2^-24 each.  O is therefore moved every kFlush tiles into fp32 sums in shared
@@ -154,15 +154,18 @@ struct Seq {
   int np, rl, dl;
   int ntp, nt, nrt;  // page tiles, tiles, row tiles
 };
+__device__ __forceinline__ void seq_tiles_of(const TreeParams& p, Seq& s) {
+  s.ntp = (s.np * p.P + 127) / 128;
+  s.nt = s.ntp + (s.rl + s.dl + 127) / 128;
+  s.nrt = (s.dl * p.gqa + 127) / 128;
+}
 __device__ __forceinline__ bool seq_load(const TreeParams& p, int b, Seq& s) {
   s.np = __ldcg(p.num_pages + b);
   s.rl = __ldcg(p.res_len + b);
   s.dl = __ldcg(p.draft_len + b);
   const bool ok = s.np >= 0 && s.np <= p.max_pages && s.rl >= 0 && s.rl <= p.P && s.dl >= 0 && s.dl <= p.T;
   if (!ok) s.np = s.rl = s.dl = 0;
-  s.ntp = (s.np * p.P + 127) / 128;
-  s.nt = s.ntp + (s.rl + s.dl + 127) / 128;
-  s.nrt = (s.dl * p.gqa + 127) / 128;
+  seq_tiles_of(p, s);
   return ok;
 }
 __device__ __forceinline__ int seq_tiles(const TreeParams& p, const Seq& s) { return s.nrt * s.nt * p.Hkv; }
@@ -173,10 +176,14 @@ struct Walk {
   int b, h, r, k;  // sequence, kv head, row tile, tile of the unit
   int pos, end;
   bool first;        // of this CTA's part of the unit
-  __device__ __forceinline__ void start(const TreeParams& p, int b0, int base, int from, int to) {
-    b = b0;
-    seq_load(p, b, s);
-    const int off = from - base, u = off / s.nt;
+  template <typename L>
+  __device__ __forceinline__ void start(const TreeParams& p, const L& ln, int from, int to) {
+    b = ln.b0;
+    s.np = ln.np;
+    s.rl = ln.rl;
+    s.dl = ln.dl;
+    seq_tiles_of(p, s);
+    const int off = from - ln.base0, u = off / s.nt;
     k = off - u * s.nt;
     h = u / s.nrt;
     r = u - h * s.nrt;
@@ -204,20 +211,31 @@ struct Walk {
   __device__ __forceinline__ bool raw() const { return k >= s.ntp; }
 };
 
-// Range of CTA i of n over W tiles, and the CTA whose range holds tile x.
-__device__ __forceinline__ int range_at(int i, int W, int n) { return int((long long)W * i / n); }
-__device__ __forceinline__ int range_owner(int x, int W, int n) { return int(((long long)(x + 1) * n - 1) / W); }
+// Range of CTA i of n (n < 2^15) over W tiles: floor(W i / n).
+__device__ __forceinline__ int range_at(int i, int W, int n) {
+  const int q = W / n, rest = W - q * n;
+  return q * i + rest * i / n;
+}
+// The CTA whose range holds tile x.
+__device__ __forceinline__ int range_owner(int x, int W, int n) {
+  int i = min(n - 1, int(float(x) * float(n) / float(W)));
+  while (range_at(i, W, n) > x) --i;
+  while (i + 1 < n && range_at(i + 1, W, n) <= x) ++i;
+  return i;
+}
 
 // Total tiles of the line, and the sequence (with its first tile) that holds tile range_at(
 // cta): every thread of a block of NT threads takes part.
 struct Line {
   int W, n, b0, base0;
+  int np, rl, dl;  // of sequence b0
   int sums[32];
 };
 template <int NT>
 __device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta, int ctas, bool flag) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int total = 0, x = 0, incl = 0;
+  Seq s;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     int run = 0, at = 0;
@@ -235,7 +253,6 @@ __device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta
       if (pass == 0 || p.batch > NT) {  // (with a sequence a thread its tiles and their sums stay)
         x = 0;
         if (b < p.batch) {
-          Seq s;
           if (!seq_load(p, b, s) && flag && pass == 0) flag_error(p.err, KVQ_DEV_ERR_LENGTH);
           x = seq_tiles(p, s);
         }
@@ -258,6 +275,9 @@ __device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta
       if (pass == 1 && x > 0 && before + incl - x <= at && at < before + incl) {
         ln.b0 = b;
         ln.base0 = before + incl - x;
+        ln.np = s.np;
+        ln.rl = s.rl;
+        ln.dl = s.dl;
       }
       if (p.batch > NT) __syncthreads();
     }
@@ -548,7 +568,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   const int W = sh.line.W, n_ctas = sh.line.n, cta = blockIdx.x;
   const bool idle = cta >= n_ctas;
   Walk wk;
-  if (!idle) wk.start(p, sh.line.b0, sh.line.base0, range_at(cta, W, n_ctas), range_at(cta + 1, W, n_ctas));
+  if (!idle) wk.start(p, sh.line, range_at(cta, W, n_ctas), range_at(cta + 1, W, n_ctas));
+  if (tid == 0 && cta > 0) {
+    // where this range's first boundary cuts a unit, and is the first to do so, merge_kernel joins its parts
+    int4 cut = make_int4(-1, 0, 0, 0);
+    if (!idle && wk.k > 0) {
+      const int c0 = range_owner(wk.pos - wk.k, W, n_ctas);
+      if (c0 == cta - 1) cut = make_int4(wk.b, wk.h * wk.s.nrt + wk.r, c0, range_owner(wk.pos - wk.k + wk.s.nt - 1, W, n_ctas));
+    }
+    p.cuts[cta] = cut;
+  }
   const int PPT = 128 / p.P;  // pages of a tile
   const uint32_t stage_bytes = uint32_t(PPT) * p.L.record;
 
@@ -582,6 +611,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           bulk_g2s(smem + kRec + st * stage_bytes + lane * p.L.record, p.pool + (size_t(id) * p.Hkv + wk.h) * p.L.record,
                    p.L.payload, &sh.rec_full[st], policy);
         ++n;
+      } else {
+        // window and drafted tokens: into L2 ahead of the dequant warps' loads
+        const int x0 = 128 * (wk.k - wk.s.ntp), nx = min(wk.s.rl + wk.s.dl, x0 + 128);
+        for (int x = x0 + lane; x < nx; x += 32) {
+          bool draft;
+          const size_t at = raw_row(p, wk.b, wk.h, wk.s.rl, x, draft);
+          const uint4* k = reinterpret_cast<const uint4*>(draft ? p.k_draft : p.res_k) + at;
+          const uint4* v = reinterpret_cast<const uint4*>(draft ? p.v_draft : p.res_v) + at;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(k));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(k + 8));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(v));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(v + 8));
+        }
       }
       more = wk.next(p);
     }
@@ -673,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   } else if (warp >= kSoftWarps) {
     // ------------------------------------------------------------ dequantization
     regs_dec<kRegsDeq>();
-    const int dw = warp - kSoftWarps, g = dw >> 1, half = dw & 1;
+    const int dw = warp - kSoftWarps, g = dw >> 2, half = (dw >> 1) & 1, a = dw & 1;
     const int pg = 32 * g / p.P, gp = g - pg * (p.P / 32);  // page of the tile, group of the page
     int it = 0, n = 0;  // tiles whose keys are written; page tiles among them
     bool more = true, ok = true, pend = false, phave = false;
@@ -683,9 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       if (!ok) return;
       const int st = (n - 1) % kRecStages;
       if (phave)
-#pragma unroll 1
-        for (int a = 0; a < 2; ++a)
-          value_codes(p, smem + kRec + st * stage_bytes + pg * p.L.record, gp, g, half, a, smem, lane);
+        value_codes(p, smem + kRec + st * stage_bytes + pg * p.L.record, gp, g, half, a, smem, lane);
       tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -704,17 +744,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const uint8_t* rec = smem + kRec + st * stage_bytes + pg * p.L.record;
         if (it > 0 && !wait_warp(sh, &sh.k_empty, uint32_t(it - 1) & 1u, p.err)) break;
         if (have)
-#pragma unroll 1
-          for (int a = 0; a < 2; ++a)
-            key_row<T, KB>(p, rec, 32 * gp + lane, 32 * g + lane, half, a, smem, sh.moves[kMoves ? st : 0][kMoves ? pg : 0]);
-        if (half == 0) {
+          key_row<T, KB>(p, rec, 32 * gp + lane, 32 * g + lane, half, a, smem, sh.moves[kMoves ? st : 0][kMoves ? pg : 0]);
+        if (half == 0 && a == 0) {
           if (have && lane < 16) {  // zero points: row 128 + g of the key operand
             const uint4 z = lds128(rec + p.L.k_zero + gp * 256 + 16 * lane);
             *reinterpret_cast<uint4*>(smem + kKhi + tco(128 + g, lane)) =
                 make_uint4(half_of(meta_h2(z.x, T())), half_of(meta_h2(z.y, T())), half_of(meta_h2(z.z, T())),
                            half_of(meta_h2(z.w, T())));
           }
-        } else {
+        } else if (half == 1 && a == 0) {
           float s = 0.0f, z = 0.0f;
           if (have) {
             const int at = 2 * value_meta_pos(32 * gp + lane);
@@ -736,14 +774,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         phave = have;
         ++n;
       } else {
-        // window and drafted tokens: warp dw takes tokens 16 dw .. 16 dw + 15 of the tile, two at
-        // a time, 16 lanes a token
+        // window and drafted tokens: warp dw takes tokens 8 dw .. 8 dw + 7 of the tile, two at a
+        // time, 16 lanes a token
         const int x0 = 128 * (wk.k - wk.s.ntp), nx = wk.s.rl + wk.s.dl, c = lane & 15;
         if (it > 0 && !wait_warp(sh, &sh.k_empty, uint32_t(it - 1) & 1u, p.err)) break;
         float top = 0.0f;
-#pragma unroll 2
-        for (int i = 0; i < 8; ++i) {
-          const int t = 16 * dw + 2 * i + (lane >> 4), x = x0 + t;
+#pragma unroll 4
+        for (int i = 0; i < 4; ++i) {
+          const int t = 8 * dw + 2 * i + (lane >> 4), x = x0 + t;
           bool draft = false, bad = false;
           uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
           if (x < nx) {
@@ -789,9 +827,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         // the values: what is no number is zero (a probability of zero has to stay zero), and
         // bf16 is brought below 2 by the token's power of two
         if (it > 0 && !wait_warp(sh, &sh.v_empty, uint32_t(it - 1) & 1u, p.err)) break;
-#pragma unroll 2
-        for (int i = 0; i < 8; ++i) {
-          const int t = 16 * dw + 2 * i + (lane >> 4), x = x0 + t;
+#pragma unroll 4
+        for (int i = 0; i < 4; ++i) {
+          const int t = 8 * dw + 2 * i + (lane >> 4), x = x0 + t;
           uint4 vx = make_uint4(0u, 0u, 0u, 0u);
           if (x < nx) {
             bool draft;
@@ -1095,42 +1133,38 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   if (warp == kIssuer) tc::dealloc(tm, 512);
 }
 
-// Joins the parts of the units that range boundary blockIdx.x + 1 cuts, 16 rows a block.
-template <typename T>
-__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ TreeParams p) {
-  __shared__ Line line;
+// Joins the parts of the units that were cut (cuts[i], i = 1 .. n_ctas - 1), 16 rows a block.
+static __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ TreeParams p) {
   pdl_wait();
   pdl_trigger();
-  const int cta = blockIdx.x + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  line_find<256>(p, line, cta, p.n_ctas, false);
-  const int W = line.W, n = line.n;
-  if (cta >= n) return;
-  Walk wk;
-  const int at = range_at(cta, W, n);
-  wk.start(p, line.b0, line.base0, at, at + 1);
-  if (wk.k == 0) return;  // the boundary falls between units
-  const int u0 = at - wk.k, c0 = range_owner(u0, W, n), c1 = range_owner(u0 + wk.s.nt - 1, W, n);
-  if (cta != c0 + 1) return;  // the unit's first boundary joins it
-  for (int r = 16 * blockIdx.y + warp; r < 16 * blockIdx.y + 16; r += 8) {
-    const int R = 128 * wk.r + r, i = R / p.gqa;
-    if (i >= wk.s.dl) return;
+  const int4 cut = __ldcg(reinterpret_cast<const int4*>(p.cuts) + blockIdx.x + 1);
+  if (cut.x < 0) return;
+  const int b = cut.x, c0 = cut.z, c1 = cut.w, lane = threadIdx.x & 31;
+  const int dl = __ldcg(p.draft_len + b), nrt = (dl * p.gqa + 127) / 128, h = cut.y / nrt, rt = cut.y - h * nrt;
+  for (int r = 16 * blockIdx.y + (threadIdx.x >> 5); r < 16 * blockIdx.y + 16; r += 8) {
+    const int R = 128 * rt + r, i = R / p.gqa;
+    if (i >= dl) return;
+    const float* part = p.part + size_t(r) * kPart;
+    constexpr size_t kSlot = 128 * kPart;
     float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part + (size_t(2 * c + (c == c0)) * 128 + r) * kPart + 128));
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(part + size_t(2 * c + (c == c0)) * kSlot + 128));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
     float l = 0.0f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int c = c0; c <= c1; ++c) {
-      const float* part = p.part + (size_t(2 * c + (c == c0)) * 128 + r) * kPart;
-      const float f = M == -INFINITY ? 0.0f : ex2(__ldcg(part + 128) - M);
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(part) + lane);
-      l = fmaf(f, __ldcg(part + 129), l);
+      const float* pc = part + size_t(2 * c + (c == c0)) * kSlot;
+      const float f = M == -INFINITY ? 0.0f : ex2(__ldcg(pc + 128) - M);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(pc) + lane);
+      l = fmaf(f, __ldcg(pc + 129), l);
       o.x = fmaf(f, x.x, o.x);
       o.y = fmaf(f, x.y, o.y);
       o.z = fmaf(f, x.z, o.z);
       o.w = fmaf(f, x.w, o.w);
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const size_t row = (size_t(wk.b) * p.T + i) * p.Hq + wk.h * p.gqa + (R - i * p.gqa);
+    const size_t row = (size_t(b) * p.T + i) * p.Hq + h * p.gqa + (R - i * p.gqa);
     reinterpret_cast<float4*>(p.out + row * kHeadDim)[lane] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   }
 }
@@ -1154,7 +1188,7 @@ cudaError_t launch_t(const TreeParams& p, cudaStream_t stream) {
   if (r < kRegsLaunch) return cudaErrorInvalidConfiguration;
   e = launch_pdl(tree_kernel<T, KB>, dim3(p.n_ctas), dim3(kThreads), size_t(bytes), stream, p);
   if (e != cudaSuccess || p.n_ctas < 2) return e;
-  return launch_pdl(merge_kernel<T>, dim3(p.n_ctas - 1, 8), dim3(256), 0, stream, p);
+  return launch_pdl(merge_kernel, dim3(p.n_ctas - 1, 8), dim3(256), 0, stream, p);
 }
 
 template <typename T>
