@@ -114,6 +114,41 @@ __device__ __forceinline__ void st8(uint32_t a, uint32_t r0, uint32_t r1, uint32
   asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
                : "memory");
 }
+// 32 columns: column 4 c + i % 4 in r[2 c] (row i / 4) and r[2 c + 1].
+__device__ __forceinline__ void st32x4(uint32_t a, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Two fp32 values in one 64-bit register: sm_100 adds, multiplies and fuses them in one
+// instruction.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 f2_get(uint64_t x) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(x));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
   return fmaxf(x, __shfl_xor_sync(kFull, x, 2));
@@ -492,37 +527,35 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x, uint32_t expo, bool& bad
 // ---------------------------------------------------------------- softmax
 
 // 32 logits of the lane's two rows at columns tR .. tR + 31, as 2^(cl S + off), times the
-// tokens' value scales, back in the same columns as fp16 high and low parts: every 16 tokens
-// in 8 + 8 columns.  sz: {s, s', z, z'} of the tokens' pairs, from the lane's first on.  The
-// sums (also with z) go to l and zs.
-__device__ __forceinline__ void weights(uint32_t tR, const float (&cl)[2], const float (&off)[2], const float4* sz,
-                                        float (&l)[2], float (&zs)[2]) {
-  uint32_t x[16];
+// tokens' value scales, back in the same columns as fp16: 16 columns of high parts, 16 of low
+// parts.  sz: {s, s', z, z'} of the tokens' pairs, from the lane's first on.  The sums (also
+// with z) go to l and zs.
+__device__ __forceinline__ void weights(uint32_t tR, const uint64_t (&cl)[2], const uint64_t (&off)[2], const float4* sz,
+                                        uint64_t (&l)[2], uint64_t (&zs)[2]) {
+  const uint64_t neg = f2(-1.0f, -1.0f);
+  uint32_t x[16], out[16];
   ld32(tR, x);
 #pragma unroll
-  for (int c = 0; c < 4; c += 2) {  // 16 tokens
-    uint32_t hi[2][2], lo[2][2];    // [8 tokens][row]
+  for (int c = 0; c < 4; ++c) {  // 8 tokens
+    const float4 v = sz[4 * c];
+    const uint64_t s2 = f2(v.x, v.y), z2 = f2(v.z, v.w);
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      const float4 v = sz[4 * (c + d)];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float p0 = ex2(__fmaf_rn(__uint_as_float(x[4 * (c + d) + 2 * r]), cl[r], off[r]));
-        float p1 = ex2(__fmaf_rn(__uint_as_float(x[4 * (c + d) + 2 * r + 1]), cl[r], off[r]));
-        l[r] += p0 + p1;
-        zs[r] = fmaf(p0, v.z, zs[r]);
-        zs[r] = fmaf(p1, v.w, zs[r]);
-        p0 *= v.x;
-        p1 *= v.y;
-        const uint32_t h = pack_h2(p0, p1);
-        const float2 f = __half22float2(u32_as_h2(h));
-        hi[d][r] = h;
-        lo[d][r] = pack_h2(p0 - f.x, p1 - f.y);
-      }
+    for (int r = 0; r < 2; ++r) {
+      const float2 t =
+          f2_get(f2_fma(f2(__uint_as_float(x[4 * c + 2 * r]), __uint_as_float(x[4 * c + 2 * r + 1])), cl[r], off[r]));
+      uint64_t p = f2(ex2(t.x), ex2(t.y));
+      l[r] = f2_add(l[r], p);
+      zs[r] = f2_fma(p, z2, zs[r]);
+      p = f2_mul(p, s2);
+      const float2 y = f2_get(p);
+      const uint32_t h = pack_h2(y.x, y.y);
+      const float2 f = __half22float2(u32_as_h2(h));
+      const float2 e = f2_get(f2_fma(f2(f.x, f.y), neg, p));
+      out[2 * c + r] = h;
+      out[8 + 2 * c + r] = pack_h2(e.x, e.y);
     }
-    st8(tR + 8 * c, hi[0][0], hi[0][1], hi[1][0], hi[1][1]);
-    st8(tR + 8 * c + 8, lo[0][0], lo[0][1], lo[1][0], lo[1][1]);
   }
+  st32x4(tR, out);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -567,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   const uint32_t tm = __shfl_sync(kFull, sh.tmem, 0);
   const int W = sh.line.W, n_ctas = sh.line.n, cta = blockIdx.x;
   const bool idle = cta >= n_ctas;
-  Walk wk;
+  Walk wk{};
   if (!idle) wk.start(p, sh.line, range_at(cta, W, n_ctas), range_at(cta + 1, W, n_ctas));
   if (tid == 0 && cta > 0) {
     // where this range's first boundary cuts a unit, and is the first to do so, merge_kernel joins its parts
@@ -652,8 +685,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const uint32_t step = praw ? 4096 / 16 : 256 / 16, id = praw ? kIdMn : kIdLo;
 #pragma unroll 1
         for (uint32_t s = 0; s < 8; ++s) {
-          tc::mma(tm + kColO, tP + 16 * s, b0 + s * step, id, s > 0 || !pfresh);
-          tc::mma(tm + kColO, tP + 16 * s + 8, b0 + s * step, id, 1u);
+          const uint32_t a = tP + 32 * (s >> 1) + 8 * (s & 1);
+          tc::mma(tm + kColO, a, b0 + s * step, id, s > 0 || !pfresh);
+          tc::mma(tm + kColO, a + 16, b0 + s * step, id, 1u);
         }
         tc::commit(&sh.v_empty);
         tc::commit(&sh.pv_done[j & 1]);
@@ -1074,19 +1108,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         // second pass
         const float4* sz = &sh.sz[v3][quad];
-        float tl[2] = {0.0f, 0.0f}, tz[2] = {0.0f, 0.0f};
+        uint64_t tl[2] = {0ull, 0ull}, tz[2] = {0ull, 0ull};
+        const uint64_t cl2[2] = {f2(cl[0], cl[0]), f2(cl[1], cl[1])};
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {
-          float off[2];
+          uint64_t off[2];
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-            off[r] = fmaf(__shfl_sync(kFull, __uint_as_float(zr[r]), (lane & ~3) + g), cl[r], nm[r]);
-          weights(tS + 32 * g, cl, off, sz + 16 * g, tl, tz);
+          for (int r = 0; r < 2; ++r) {
+            const float o = fmaf(__shfl_sync(kFull, __uint_as_float(zr[r]), (lane & ~3) + g), cl[r], nm[r]);
+            off[r] = f2(o, o);
+          }
+          weights(tS + 32 * g, cl2, off, sz + 16 * g, tl, tz);
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          l[r] += tl[r];
-          zs[r] += tz[r];
+          const float2 a = f2_get(tl[r]), z = f2_get(tz[r]);
+          l[r] += a.x + a.y;
+          zs[r] += z.x + z.y;
         }
         const bool flush = run > 0 && run % kFlush == 0;
         if (flush || (run > 0 && __any_sync(kFull, alpha[0] != 1.0f || alpha[1] != 1.0f))) {
