@@ -466,6 +466,8 @@ kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t p
   p.max_pages = max_pages;
   p.T = n_draft;
   p.W = (n_draft + 31) / 32;
+  p.gqa_log2 = p.gqa == 8 ? 3 : p.gqa == 4 ? 2 : p.gqa == 2 ? 1 : 0;
+  p.gpp_log2 = p.P == 128 ? 2 : p.P == 64 ? 1 : 0;
   p.L = make_layout(cfg->page_tokens, cfg->head_dim, cfg->num_boost, cfg->key_group);
   p.q = static_cast<const uint16_t*>(q);
   p.page_table = page_table;

@@ -374,6 +374,7 @@ struct TreeParams {
   long long pool_pages;
   int Hkv, Hq, gqa, P, k, batch, max_pages;
   int T, W;  // drafted tokens, 32-bit mask words a token
+  int gqa_log2, gpp_log2;  // of gqa and of the 32-token groups of a page
   Layout L;
   const uint16_t* q;  // [batch][T][Hq][128]
   const int32_t* page_table;

@@ -180,6 +180,14 @@ __device__ __forceinline__ uint32_t meta_h2(uint32_t x, __nv_bfloat16) {
   const float2 f = unpack2(x, __nv_bfloat16());
   return pack_h2(f.x, f.y);
 }
+// A pair of the cache dtype times a power of two f, as fp16.
+__device__ __forceinline__ uint32_t scaled_h2(uint32_t x, float f, __half) {
+  return h2_as_u32(__hmul2(u32_as_h2(x), __float2half2_rn(f)));
+}
+__device__ __forceinline__ uint32_t scaled_h2(uint32_t x, float f, __nv_bfloat16) {
+  const float2 y = unpack2(x, __nv_bfloat16());
+  return pack_h2(y.x * f, y.y * f);
+}
 __device__ __forceinline__ uint32_t half_of(uint32_t x) {  // x / 2 of an fp16 pair
   return h2_as_u32(__hmul2(u32_as_h2(x), __float2half2_rn(0.5f)));
 }
@@ -190,9 +198,9 @@ struct Seq {
   int ntp, nt, nrt;  // page tiles, tiles, row tiles
 };
 __device__ __forceinline__ void seq_tiles_of(const TreeParams& p, Seq& s) {
-  s.ntp = (s.np * p.P + 127) / 128;
-  s.nt = s.ntp + (s.rl + s.dl + 127) / 128;
-  s.nrt = (s.dl * p.gqa + 127) / 128;
+  s.ntp = (s.np * p.P + 127) >> 7;
+  s.nt = s.ntp + ((s.rl + s.dl + 127) >> 7);
+  s.nrt = ((s.dl << p.gqa_log2) + 127) >> 7;
 }
 __device__ __forceinline__ bool seq_load(const TreeParams& p, int b, Seq& s) {
   s.np = __ldcg(p.num_pages + b);
@@ -343,28 +351,26 @@ struct Shared {
   __align__(16) Moves moves[MOVES ? kRecStages : 1][MOVES ? 4 : 1];  // [stage][page of the tile]
 };
 
-// Waits for a phase (about a second at most); false once any wait of the CTA has given up.
+// Waits for a phase (about a second at most); false once any wait of the CTA has given up,
+// which the end of the kernel reports.
 template <typename S>
-__device__ __forceinline__ bool wait(S& sh, uint64_t* bar, uint32_t parity, int32_t* err) {
+__device__ __forceinline__ bool wait(S& sh, uint64_t* bar, uint32_t parity) {
   bool ok = mbar_try_wait_suspend(bar, parity, 20000u);
   if (!ok) {
     const uint32_t t0 = uint32_t(clock());
     volatile int* abort = &sh.abort;
     do {
-      if (*abort) return false;
+      if (*abort) break;
       ok = mbar_try_wait_suspend(bar, parity, 20000u);
     } while (!ok && uint32_t(clock()) - t0 < (1u << 31));
-    if (!ok) {
-      flag_error(err, KVQ_DEV_ERR_TIMEOUT);
-      *abort = 1;
-    }
+    if (!ok) *abort = 1;
   }
   return ok;
 }
 // The same by a whole warp, with one answer for all lanes.
 template <typename S>
-__device__ __forceinline__ bool wait_warp(S& sh, uint64_t* bar, uint32_t parity, int32_t* err) {
-  return __all_sync(kFull, wait(sh, bar, parity, err));
+__device__ __forceinline__ bool wait_warp(S& sh, uint64_t* bar, uint32_t parity) {
+  return __all_sync(kFull, wait(sh, bar, parity));
 }
 
 constexpr int kPart = 132;  // floats of a partial row: unnormalised output, reference M, sum
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
     p.cuts[cta] = cut;
   }
-  const int PPT = 128 / p.P;  // pages of a tile
+  const int PPT = 4 >> p.gpp_log2;  // pages of a tile
   const uint32_t stage_bytes = uint32_t(PPT) * p.L.record;
 
   if (idle) {
@@ -624,6 +630,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     int n = 0;
     bool more = true;
     while (more) {
+      if (wk.first)  // the unit's query rows into L2
+        for (int i = lane; i < 128; i += 32) {
+          const int R = 128 * wk.r + i, t = R >> p.gqa_log2;
+          if (t < wk.s.dl) {
+            const uint16_t* q = p.q + ((size_t(wk.b) * p.T + t) * p.Hq + (wk.h << p.gqa_log2) + (R - (t << p.gqa_log2))) * kHeadDim;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+          }
+        }
       if (!wk.raw()) {
         const int st = n % kRecStages, npg = min(PPT, wk.s.np - wk.k * PPT);
         int id = 0;
@@ -634,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             id = 0;
           }
         }
-        if (n >= kRecStages && !wait_warp(sh, &sh.rec_empty[st], uint32_t(n / kRecStages - 1) & 1u, p.err)) break;
+        if (n >= kRecStages && !wait_warp(sh, &sh.rec_empty[st], uint32_t(n / kRecStages - 1) & 1u)) break;
         if (lane == 0) {
           tc::fence_async_smem();
           mbar_arrive_expect_tx(&sh.rec_full[st], uint32_t(npg) * p.L.payload);
@@ -670,63 +685,68 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const uint32_t sKh = smem_addr(smem + kKhi), sKl = smem_addr(smem + kKlo), sV = smem_addr(smem + kV);
     constexpr uint32_t kIdHi = tc::idesc_f16(144, false, false), kIdLo = tc::idesc_f16(128, false, false),
                        kIdMn = tc::idesc_f16(128, false, true);
-    int it = 0, seg = 0;
+    // QK of tile `it`, one tile ahead of PV of tile j; at a unit's first tile PV catches up
+    // first, because the new query waits for the rows of the old one to be done with S
+    int it = 0, j = 0, seg = 0, run = 0;  // run: tiles of this CTA's part of the unit so far
     bool more = true, ok = true;
-    bool praw = false, pfresh = false;  // the tile before: raw; O starts anew with it
-    auto second = [&](int j) {          // O += P V of tile j
-      const uint32_t tP = tm + uint32_t(j & 1) * kColS;
-      ok = ok && wait_warp(sh, &sh.p_full[j & 1], uint32_t(j >> 1) & 1u, p.err) &&
-           wait_warp(sh, &sh.v_full, uint32_t(j) & 1u, p.err);
-      if (!ok) return;
-      tc::fence_after();
-      if (elect_one()) {
-        // 16 tokens a step: the raw tile's rows are tokens (MN-major), the codes' are channels
-        const uint64_t b0 = praw ? tc::smem_desc(sV, 2048, 128) : tc::smem_desc(sV, 128, 2048);
-        const uint32_t step = praw ? 4096 / 16 : 256 / 16, id = praw ? kIdMn : kIdLo;
-#pragma unroll 1
-        for (uint32_t s = 0; s < 8; ++s) {
-          const uint32_t a = tP + 32 * (s >> 1) + 8 * (s & 1);
-          tc::mma(tm + kColO, a, b0 + s * step, id, s > 0 || !pfresh);
-          tc::mma(tm + kColO, a + 16, b0 + s * step, id, 1u);
-        }
-        tc::commit(&sh.v_empty);
-        tc::commit(&sh.pv_done[j & 1]);
-      }
-      __syncwarp();
-    };
-    int run = 0;  // tiles of this CTA's part of the unit so far
-    while (more && ok) {
+    uint32_t raws = 0, fresh = 0;  // by the tile's parity: raw; O starts anew with it
+    while (true) {
       const bool first = __any_sync(kFull, wk.first), raw = __any_sync(kFull, wk.raw());  // the same in all lanes
-      if (first) {
-        if (it > 0) second(it - 1);
-        ok = ok && wait_warp(sh, &sh.q_full, uint32_t(seg++) & 1u, p.err);
-        run = 0;
-      }
-      ok = ok && wait_warp(sh, &sh.k_full, uint32_t(it) & 1u, p.err);
-      if (!ok) break;
-      tc::fence_after();
-      const uint32_t dS = tm + uint32_t(it & 1) * kColS;
-      if (elect_one()) {
-        const uint64_t bh = tc::smem_desc(sKh, 128, 2048), bl = tc::smem_desc(sKl, 128, 2048);
-#pragma unroll 1
-        for (uint32_t s = 0; s < 8; ++s) tc::mma(dS, tm + kColQ + 8 * s, bh + s * (256 / 16), kIdHi, s > 0);
-        if (!raw) {
-#pragma unroll 1
-          for (uint32_t s = 0; s < 8; ++s) tc::mma(dS, tm + kColQ + 8 * s, bl + s * (256 / 16), kIdLo, 1u);
+      if (more && it - j < (first ? 1 : 2)) {
+        if (first) {
+          ok = ok && wait_warp(sh, &sh.q_full, uint32_t(seg++) & 1u);
+          run = 0;
         }
-        tc::commit(&sh.k_empty);
-        tc::commit(&sh.s_full[it & 1]);
+        ok = ok && wait_warp(sh, &sh.k_full, uint32_t(it) & 1u);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t dS = tm + uint32_t(it & 1) * kColS;
+        if (elect_one()) {
+          uint64_t bd = tc::smem_desc(sKh, 128, 2048);
+          const int steps = raw ? 8 : 16;
+#pragma unroll 1
+          for (int s = 0; s < steps; ++s) {
+            if (s == 8) bd = tc::smem_desc(sKl, 128, 2048);  // the remainders
+            tc::mma(dS, tm + kColQ + 8 * (s & 7), bd, s < 8 ? kIdHi : kIdLo, s > 0);
+            bd += 256 / 16;
+          }
+          tc::commit(&sh.k_empty);
+          tc::commit(&sh.s_full[it & 1]);
+        }
+        __syncwarp();
+        const uint32_t bit = 1u << (it & 1);
+        raws = raw ? raws | bit : raws & ~bit;
+        fresh = run++ % kFlush == 0 ? fresh | bit : fresh & ~bit;
+        ++it;
+        more = __any_sync(kFull, wk.next(p));
+      } else if (j < it) {
+        const uint32_t tP = tm + uint32_t(j & 1) * kColS;
+        ok = ok && wait_warp(sh, &sh.p_full[j & 1], uint32_t(j >> 1) & 1u) && wait_warp(sh, &sh.v_full, uint32_t(j) & 1u);
+        if (!ok) break;
+        tc::fence_after();
+        const bool praw = (raws >> (j & 1)) & 1u, pfresh = (fresh >> (j & 1)) & 1u;
+        if (elect_one()) {
+          // 16 tokens a step: the raw tile's rows are tokens (MN-major), the codes' are channels
+          uint64_t bd = praw ? tc::smem_desc(sV, 2048, 128) : tc::smem_desc(sV, 128, 2048);
+          const uint32_t step = praw ? 4096 / 16 : 256 / 16, id = praw ? kIdMn : kIdLo;
+#pragma unroll 1
+          for (uint32_t s = 0; s < 8; ++s) {
+            const uint32_t a = tP + 32 * (s >> 1) + 8 * (s & 1);
+            tc::mma(tm + kColO, a, bd, id, s > 0 || !pfresh);
+            tc::mma(tm + kColO, a + 16, bd, id, 1u);
+            bd += step;
+          }
+          tc::commit(&sh.v_empty);
+          tc::commit(&sh.pv_done[j & 1]);
+        }
+        __syncwarp();
+        ++j;
+      } else {
+        break;
       }
-      __syncwarp();
-      if (!first) second(it - 1);
-      praw = raw;
-      pfresh = run++ % kFlush == 0;
-      ++it;
-      more = __any_sync(kFull, wk.next(p));
     }
-    if (ok) second(it - 1);
     // the products have completed before the operands' memory is released
-    if (ok) wait_warp(sh, &sh.pv_done[(it - 1) & 1], uint32_t((it - 1) >> 1) & 1u, p.err);
+    if (ok && j > 0) wait_warp(sh, &sh.pv_done[(j - 1) & 1], uint32_t((j - 1) >> 1) & 1u);
     } else if (kMoves && warp == kMover) {
       // ---------------------------------------------------------- moves of boosted codes
       if constexpr (kMoves) {
@@ -736,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           if (!wk.raw()) {
             const int st = n % kRecStages, npg = min(PPT, wk.s.np - wk.k * PPT);
             // (a stage that is full again has been read out, its moves too)
-            if (!wait_warp(sh, &sh.rec_full[st], uint32_t(n / kRecStages) & 1u, p.err)) break;
+            if (!wait_warp(sh, &sh.rec_full[st], uint32_t(n / kRecStages) & 1u)) break;
             for (int i = 0; i < npg; ++i)
               list_moves<KB>(smem + kRec + st * stage_bytes + i * p.L.record + p.L.boost_idx, sh.moves[st][i], lane);
             if (lane == 0) mbar_arrive(&sh.mv_full[st]);
@@ -750,12 +770,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     // ------------------------------------------------------------ dequantization
     regs_dec<kRegsDeq>();
     const int dw = warp - kSoftWarps, g = dw >> 2, half = (dw >> 1) & 1, a = dw & 1;
-    const int pg = 32 * g / p.P, gp = g - pg * (p.P / 32);  // page of the tile, group of the page
+    const int pg = g >> p.gpp_log2, gp = g - (pg << p.gpp_log2);  // page of the tile, group of the page
     int it = 0, n = 0;  // tiles whose keys are written; page tiles among them
     bool more = true, ok = true, pend = false, phave = false;
     // the values of the page tile before, whose record is in stage (n - 1) % kRecStages
     auto values = [&](int j) {
-      if (j > 0) ok = wait_warp(sh, &sh.v_empty, uint32_t(j - 1) & 1u, p.err);
+      if (j > 0) ok = wait_warp(sh, &sh.v_empty, uint32_t(j - 1) & 1u);
       if (!ok) return;
       const int st = (n - 1) % kRecStages;
       if (phave)
@@ -772,11 +792,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const int v3 = it % 3;
       if (!wk.raw()) {
         const int st = n % kRecStages;
-        if (kMoves && !wait_warp(sh, &sh.mv_full[st], uint32_t(n / kRecStages) & 1u, p.err)) break;
-        if (!wait_warp(sh, &sh.rec_full[st], uint32_t(n / kRecStages) & 1u, p.err)) break;
+        if (kMoves && !wait_warp(sh, &sh.mv_full[st], uint32_t(n / kRecStages) & 1u)) break;
+        if (!wait_warp(sh, &sh.rec_full[st], uint32_t(n / kRecStages) & 1u)) break;
         const bool have = pg < wk.s.np - wk.k * PPT;
         const uint8_t* rec = smem + kRec + st * stage_bytes + pg * p.L.record;
-        if (it > 0 && !wait_warp(sh, &sh.k_empty, uint32_t(it - 1) & 1u, p.err)) break;
+        if (it > 0 && !wait_warp(sh, &sh.k_empty, uint32_t(it - 1) & 1u)) break;
         if (have)
           key_row<T, KB>(p, rec, 32 * gp + lane, 32 * g + lane, half, a, smem, sh.moves[kMoves ? st : 0][kMoves ? pg : 0]);
         if (half == 0 && a == 0) {
@@ -810,41 +830,60 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       } else {
         // window and drafted tokens: warp dw takes tokens 8 dw .. 8 dw + 7 of the tile, two at a
         // time, 16 lanes a token
-        const int x0 = 128 * (wk.k - wk.s.ntp), nx = wk.s.rl + wk.s.dl, c = lane & 15;
-        if (it > 0 && !wait_warp(sh, &sh.k_empty, uint32_t(it - 1) & 1u, p.err)) break;
-        float top = 0.0f;
-#pragma unroll 4
-        for (int i = 0; i < 4; ++i) {
-          const int t = 8 * dw + 2 * i + (lane >> 4), x = x0 + t;
-          bool draft = false, bad = false;
-          uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
-          if (x < nx) {
-            const size_t at = raw_row(p, wk.b, wk.h, wk.s.rl, x, draft) + c;
-            kx = __ldcg(reinterpret_cast<const uint4*>(draft ? p.k_draft : p.res_k) + at);
-            vx = __ldcg(reinterpret_cast<const uint4*>(draft ? p.v_draft : p.res_v) + at);
-          }
-          uint32_t k[4] = {kx.x, kx.y, kx.z, kx.w};
-          const uint32_t v[4] = {vx.x, vx.y, vx.z, vx.w};
-          float m = 0.0f;
+        const int x0 = 128 * (wk.k - wk.s.ntp) + 8 * dw + (lane >> 4), nx = wk.s.rl + wk.s.dl, c = lane & 15;
+        const int t0 = 8 * dw + (lane >> 4);  // token of the tile, and the 3 that follow it two by two
+        auto rows = [&](const uint16_t* window, const uint16_t* drafted, uint4 (&x)[4]) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack2(k[e], T());
-            k[e] = pack_h2(0.5f * f.x, 0.5f * f.y);
-            const float2 y = unpack2(finite2(v[e], BF ? 0x7f80u : 0x7c00u, bad), T());
-            m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
+          for (int i = 0; i < 4; ++i) {
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (x0 + 2 * i < nx) {
+              bool draft;
+              const size_t at = raw_row(p, wk.b, wk.h, wk.s.rl, x0 + 2 * i, draft) + c;
+              x[i] = __ldcg(reinterpret_cast<const uint4*>(draft ? drafted : window) + at);
+            }
           }
+        };
+        uint4 x[4];
+        rows(p.res_k, p.k_draft, x);
+        if (it > 0 && !wait_warp(sh, &sh.k_empty, uint32_t(it - 1) & 1u)) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t k[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint8_t* dst = smem + kKhi + tco(t0 + 2 * i, c & ~3) + 4 * (c & 3);
 #pragma unroll
           for (int e = 0; e < 4; ++e)  // pair e of 8 channels c: the operand's order
-            *reinterpret_cast<uint32_t*>(smem + kKhi + tco(t, (c & ~3) + e) + 4 * (c & 3)) = k[e];
-          if (bad && (!draft || seen_by_any(p, wk.b, wk.s.dl, x - wk.s.rl))) flag_error(p.err, KVQ_DEV_ERR_RANGE);
-          float s = 0.5f;
-          if constexpr (BF) {  // the power of two below the token's largest value
+            *reinterpret_cast<uint32_t*>(dst + 128 * e) = scaled_h2(k[e], 0.5f, T());
+        }
+        // the values: what is no number is zero (a probability of zero has to stay zero), and
+        // bf16 is brought below 2 by the token's power of two
+        rows(p.res_v, p.v_draft, x);
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int xi = x0 + 2 * i;
+          uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          bool bad = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = finite2(v[e], BF ? 0x7f80u : 0x7c00u, bad);
+          if (bad && (xi < wk.s.rl || seen_by_any(p, wk.b, wk.s.dl, xi - wk.s.rl))) flag_error(p.err, KVQ_DEV_ERR_RANGE);
+          float s = xi < nx ? 0.5f : 0.0f;
+          if constexpr (BF) {
+            float m = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 y = unpack2(v[e], T());
+              m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
+            }
 #pragma unroll
             for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-            s = 0.5f * pow2i(max(-90, min(100, int((__float_as_uint(m) >> 23) & 0xff) - 127)));
+            const int e2 = max(-90, min(100, int((__float_as_uint(m) >> 23) & 0xff) - 127));
+            s *= pow2i(e2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = scaled_h2(v[e], pow2i(-e2), T());
           }
-          if (x >= nx) s = 0.0f;
+          x[i] = make_uint4(v[0], v[1], v[2], v[3]);
           if (c == 0) {
+            const int t = t0 + 2 * i;
             float* sz = reinterpret_cast<float*>(sh.sz[v3]) + 4 * (t >> 1) + (t & 1);
             sz[0] = s;
             sz[2] = 0.0f;
@@ -858,31 +897,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (lane == 0) mbar_arrive(&sh.k_full);
         if (pend) values(it - 1);
         if (!ok) break;
-        // the values: what is no number is zero (a probability of zero has to stay zero), and
-        // bf16 is brought below 2 by the token's power of two
-        if (it > 0 && !wait_warp(sh, &sh.v_empty, uint32_t(it - 1) & 1u, p.err)) break;
-#pragma unroll 4
-        for (int i = 0; i < 4; ++i) {
-          const int t = 8 * dw + 2 * i + (lane >> 4), x = x0 + t;
-          uint4 vx = make_uint4(0u, 0u, 0u, 0u);
-          if (x < nx) {
-            bool draft;
-            const size_t at = raw_row(p, wk.b, wk.h, wk.s.rl, x, draft) + c;
-            vx = __ldcg(reinterpret_cast<const uint4*>(draft ? p.v_draft : p.res_v) + at);
-          }
-          uint32_t v[4] = {vx.x, vx.y, vx.z, vx.w};
-          bool bad = false;
-          const float f = BF ? 0.5f / fmaxf(reinterpret_cast<const float*>(sh.sz[v3])[4 * (t >> 1) + (t & 1)], 1e-30f) : 1.0f;
+        if (it > 0 && !wait_warp(sh, &sh.v_empty, uint32_t(it - 1) & 1u)) break;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = finite2(v[e], BF ? 0x7f80u : 0x7c00u, bad);
-            if constexpr (BF) {
-              const float2 y = unpack2(v[e], T());
-              v[e] = pack_h2(y.x * f, y.y * f);
-            }
-          }
-          *reinterpret_cast<uint4*>(smem + kV + tco(t, c)) = make_uint4(v[0], v[1], v[2], v[3]);
-        }
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(smem + kV + tco(t0 + 2 * i, c)) = x[i];
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.v_full);
@@ -900,17 +917,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     int it = 0, run = 0, k0 = 0;  // tiles; tiles of this part of the unit, and its first
     bool some = false, to_end = false;
     bool valid[2] = {false, false};
-    int u_dl = 0, u_rl = 0;
     size_t orow[2] = {0, 0};
     float M[2], l[2], zs[2], cl[2];
     float asc[2];     // factor of the sums in shared memory against O (0: nothing there yet)
-    uint4 mk0, mk1;   // drafted tokens the rows see
     // Waits until the second product of tile j is complete.  A parity names a phase only
     // among two: with a barrier for every other tile, and tile it - 2 waited for at tile it,
     // the phase asked for is always the current one or the one before.  (After a wait that
     // gave up every other one returns at once, and the loop runs out by itself.)
     auto wait_pv = [&](int j) {
-      wait(sh, &sh.pv_done[j & 1], uint32_t(j >> 1) & 1u, p.err);
+      wait(sh, &sh.pv_done[j & 1], uint32_t(j >> 1) & 1u);
       __syncwarp();
       tc::fence_after();
     };
@@ -931,51 +946,41 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                          : p.part + (size_t(2 * cta + (k0 == 0 ? 1 : 0)) * 128 + row + 8 * r) * kPart;
         float ncl[2] = {0.0f, 0.0f};
         if (!done) {
-          some = 128 * wk.r + row0 < wk.s.dl * p.gqa;  // any row of this warp
-          u_dl = wk.s.dl;
-          u_rl = wk.s.rl;
+          some = 128 * wk.r + row0 < wk.s.dl << p.gqa_log2;  // any row of this warp
           if (some) {
-            uint32_t v[2][16];  // [row][cc][pair]: channels 8 (4 cc + quad) + 2 pair, the operand's order
+            // 16 bytes c of a row: channels 8 (4 c + quad) .., the operand's order
+            uint4 v[2][4];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const int R = 128 * wk.r + row + 8 * r, i = R / p.gqa;
+              const int R = 128 * wk.r + row + 8 * r, i = R >> p.gqa_log2;
               valid[r] = i < wk.s.dl;
-              orow[r] = (size_t(wk.b) * p.T + i) * p.Hq + wk.h * p.gqa + (R - i * p.gqa);
+              orow[r] = (size_t(wk.b) * p.T + i) * p.Hq + (wk.h << p.gqa_log2) + (R - (i << p.gqa_log2));
               const uint4* src = reinterpret_cast<const uint4*>(p.q + orow[r] * kHeadDim) + quad;
-              float m = 0.0f;
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint4 x = valid[r] ? __ldcg(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
-                v[r][4 * c] = x.x;
-                v[r][4 * c + 1] = x.y;
-                v[r][4 * c + 2] = x.z;
-                v[r][4 * c + 3] = x.w;
-              }
-              auto mask = [&](int j) {
-                const int left = u_dl - 32 * j;
-                return valid[r] && left > 0 ? __ldcg(p.mask + (size_t(wk.b) * p.T + i) * p.W + j) &
-                                                  (left >= 32 ? kFull : (1u << left) - 1u)
-                                            : 0u;
-              };
-              (r ? mk1 : mk0) = make_uint4(mask(0), mask(1), mask(2), mask(3));
+              for (int c = 0; c < 4; ++c) v[r][c] = valid[r] ? __ldcg(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            float f[2];
 #pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const float2 f = unpack2(v[r][c], T());
-                m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
-              }
-              m = quad_max(m);
+            for (int r = 0; r < 2; ++r) {
+              uint32_t m2 = 0u;  // magnitudes as integers: the order of their bits
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v[r][c].x & 0x7fff7fffu, v[r][c].y & 0x7fff7fffu),
+                                           __vmaxu2(v[r][c].z & 0x7fff7fffu, v[r][c].w & 0x7fff7fffu)));
+              const float2 m = unpack2(m2, T());
+              const float top = quad_max(fmaxf(m.x, m.y));
               // |q| < 2^e; e = 0 below 1
-              const int e = min(max(int((__float_as_uint(m) >> 23) & 0xff) - 126, 0), 126);
-              const float f = p.c_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
+              const int e = min(max(int((__float_as_uint(top) >> 23) & 0xff) - 126, 0), 126);
+              f[r] = p.c_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
               ncl[r] = fmaxf(2.0f * fabsf(p.c_log2) * pow2i(e), 1e-30f);  // above 0: a masked -inf stays one
-#pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const float2 y = unpack2(v[r][c], T());
-                v[r][c] = pack_h2(y.x * f, y.y * f);
-              }
             }
 #pragma unroll
-            for (int c = 0; c < 16; c += 2) st8(tm + kColQ + at + 4 * c, v[0][c], v[1][c], v[0][c + 1], v[1][c + 1]);
+            for (int c = 0; c < 4; ++c) {
+              st8(tm + kColQ + at + 16 * c, scaled_h2(v[0][c].x, f[0], T()), scaled_h2(v[1][c].x, f[1], T()),
+                  scaled_h2(v[0][c].y, f[0], T()), scaled_h2(v[1][c].y, f[1], T()));
+              st8(tm + kColQ + at + 16 * c + 8, scaled_h2(v[0][c].z, f[0], T()), scaled_h2(v[1][c].z, f[1], T()),
+                  scaled_h2(v[0][c].w, f[0], T()), scaled_h2(v[1][c].w, f[1], T()));
+            }
             tc::wait_st();
           }
           tc::fence_before();
@@ -985,14 +990,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (it > 0) {
           wait_pv(it - 1);
           if (some0) {
-            float inv[2];
-            bool bad = false;
+            uint64_t inv[2], z2[2], a2[2], chk = 0ull;  // chk: 0, or no number once a result is none
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               l[r] = quad_sum(l[r]);
               zs[r] = quad_sum(zs[r]);
-              inv[r] = whole ? (l[r] > 0.0f ? 1.0f / l[r] : 0.0f) : 1.0f;
-              bad |= v0[r] && !(l[r] < INFINITY);
+              const float x = whole ? (l[r] > 0.0f ? 1.0f / l[r] : 0.0f) : 1.0f;
+              inv[r] = f2(x, x);
+              z2[r] = f2(zs[r], zs[r]);
+              a2[r] = f2(asc[r], asc[r]);
+              if (v0[r]) chk = f2_fma(z2[r], 0ull, f2_fma(f2(l[r], l[r]), 0ull, chk));
             }
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
@@ -1003,14 +1010,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                   if (!v0[r]) continue;
-                  const float2 a = asc[r] != 0.0f ? sums(16 * i + 4 * c + quad, r) : make_float2(0.f, 0.f);
-                  const float x = fmaf(2.0f, fmaf(a.x, asc[r], __uint_as_float(o[4 * c + 2 * r])), zs[r]) * inv[r];
-                  const float y = fmaf(2.0f, fmaf(a.y, asc[r], __uint_as_float(o[4 * c + 2 * r + 1])), zs[r]) * inv[r];
-                  bad |= !(fabsf(x) < INFINITY) || !(fabsf(y) < INFINITY);
-                  *reinterpret_cast<float2*>(dst[r] + 32 * i + 8 * c + 2 * quad) = make_float2(x, y);
+                  uint64_t x = f2(__uint_as_float(o[4 * c + 2 * r]), __uint_as_float(o[4 * c + 2 * r + 1]));
+                  if (asc[r] != 0.0f) {
+                    const float2 a = sums(16 * i + 4 * c + quad, r);
+                    x = f2_fma(f2(a.x, a.y), a2[r], x);
+                  }
+                  x = f2_mul(f2_fma(x, f2(2.0f, 2.0f), z2[r]), inv[r]);
+                  chk = f2_fma(x, 0ull, chk);
+                  *reinterpret_cast<float2*>(dst[r] + 32 * i + 8 * c + 2 * quad) = f2_get(x);
                 }
             }
-            if (bad) flag_error(p.err, KVQ_DEV_ERR_RANGE);
+            const float2 ck = f2_get(chk);
+            if (ck.x != 0.0f || ck.y != 0.0f) flag_error(p.err, KVQ_DEV_ERR_RANGE);
 #pragma unroll
             for (int r = 0; r < 2; ++r)
               if (!whole && v0[r] && quad == 0) {
@@ -1032,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const int buf = it & 1, v3 = it % 3;
       const uint32_t tS = tm + uint32_t(buf) * kColS + at;
       const bool raw = wk.raw();
-      wait(sh, &sh.s_full[buf], uint32_t(it >> 1) & 1u, p.err);
+      wait(sh, &sh.s_full[buf], uint32_t(it >> 1) & 1u);
       if (it >= 2) wait_pv(it - 2);
       __syncwarp();
       tc::fence_after();
@@ -1041,25 +1052,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (!raw) ld4(tS + 128, zr);
         if (raw || wk.s.np - wk.k * PPT < PPT) {
           // masked places, whatever they hold, become -inf: tokens that are not there or not seen
-          const int ng = raw ? 0 : (wk.s.np - wk.k * PPT) * (p.P / 32);  // groups that hold tokens
+          const int ng = raw ? 0 : (wk.s.np - wk.k * PPT) << p.gpp_log2;  // groups that hold tokens
           if (quad >= ng) zr[0] = zr[1] = 0u;
 #pragma unroll 1
           for (int g = ng; g < 4; ++g) {
             uint32_t x[16], see[2] = {0u, 0u};
-            ld32(tS + 32 * g, x);
             if (raw) {
               // bits of the 32 tokens from token xw of the raw sequence on, the lane's first lowest
-              const int xw = 128 * (wk.k - wk.s.ntp) + 32 * g, in_window = u_rl - xw;
-              const int d = xw - u_rl, wd = d >> 5;  // d: first drafted token of the word
-              const uint32_t v = in_window >= 32 ? kFull : in_window > 0 ? (1u << in_window) - 1u : 0u;
+              const int xw = 128 * (wk.k - wk.s.ntp) + 32 * g, in_window = wk.s.rl - xw;
+              if (in_window >= 32) continue;
+              const int d = xw - wk.s.rl, wd = d >> 5;  // d: first drafted token of the word
+              const uint32_t v = in_window > 0 ? (1u << in_window) - 1u : 0u;
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                const uint4 mk = r ? mk1 : mk0;
-                const uint32_t m0 = wd == 0 ? mk.x : wd == 1 ? mk.y : wd == 2 ? mk.z : wd == 3 ? mk.w : 0u;
-                const uint32_t m1 = wd == -1 ? mk.x : wd == 0 ? mk.y : wd == 1 ? mk.z : wd == 2 ? mk.w : 0u;
-                see[r] = (v | (d > -32 ? __funnelshift_r(m0, m1, uint32_t(d) & 31u) : 0u)) >> (2 * quad);
+                const uint32_t* mask = p.mask + (size_t(wk.b) * p.T + ((128 * wk.r + row + 8 * r) >> p.gqa_log2)) * p.W;
+                auto word = [&](int j) {  // of the row's mask, without what is behind draft_len
+                  const int left = wk.s.dl - 32 * j;
+                  return valid[r] && j >= 0 && left > 0 ? __ldcg(mask + j) & (left >= 32 ? kFull : (1u << left) - 1u) : 0u;
+                };
+                see[r] = (v | __funnelshift_r(word(wd), word(wd + 1), uint32_t(d) & 31u)) >> (2 * quad);
               }
             }
+            ld32(tS + 32 * g, x);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               if (!((see[(j >> 1) & 1] >> (8 * (j >> 2) + (j & 1))) & 1u)) x[j] = 0xff800000u;
@@ -1168,6 +1182,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   tc::fence_before();
   __syncwarp();
   __syncthreads();
+  if (tid == 0 && sh.abort) flag_error(p.err, KVQ_DEV_ERR_TIMEOUT);
   if (warp == kIssuer) tc::dealloc(tm, 512);
 }
 
