@@ -62,10 +62,10 @@ constexpr int kRecStages = 3;
 // memory, which round to nearest.  (Left in tensor memory over 28 tiles of a 4096-token
 // cache, the output was off by 3.6e-5 against 64 bits.)
 constexpr int kFlush = 4;
-constexpr uint32_t kAccStride = 132 * 8;  // output sums: [column / 2][row], rows padded against bank conflicts
+constexpr uint32_t kAccStride = 544;  // bytes of an output row's sums: 128 floats, padded against bank conflicts
 // shared-memory offsets: key operand (high parts and zero points, remainders), value operand,
 // output sums, record stages
-constexpr uint32_t kKhi = 0, kKlo = 144 * 256, kV = kKlo + 128 * 256, kAcc = kV + 128 * 256, kRec = kAcc + 64 * kAccStride;
+constexpr uint32_t kKhi = 0, kKlo = 144 * 256, kV = kKlo + 128 * 256, kAcc = kV + 128 * 256, kRec = kAcc + 128 * kAccStride;
 constexpr int kColS = 144, kColO = 288, kColQ = 416;  // tensor-memory columns: S at 0 and 144
 
 __device__ __forceinline__ uint32_t tco(int r, int c) { return uint32_t((r >> 3) * 2048 + c * 128 + (r & 7) * 16); }
@@ -930,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       tc::fence_after();
     };
     auto sums = [&](int c2, int r) -> float2& {  // output sums of columns 2 c2, 2 c2 + 1
-      return *reinterpret_cast<float2*>(smem + kAcc + c2 * kAccStride + (row + 8 * r) * 8);
+      return *reinterpret_cast<float2*>(smem + kAcc + (row + 8 * r) * kAccStride + c2 * 8);
     };
     bool done = false;
     while (true) {
@@ -990,6 +990,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (it > 0) {
           wait_pv(it - 1);
           if (some0) {
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the rows before have left their place
+            __syncwarp();
             uint64_t inv[2], z2[2], a2[2], chk = 0ull;  // chk: 0, or no number once a result is none
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -1009,17 +1011,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                  if (!v0[r]) continue;
+                  float2& sum = sums(16 * i + 4 * c + quad, r);
                   uint64_t x = f2(__uint_as_float(o[4 * c + 2 * r]), __uint_as_float(o[4 * c + 2 * r + 1]));
-                  if (asc[r] != 0.0f) {
-                    const float2 a = sums(16 * i + 4 * c + quad, r);
-                    x = f2_fma(f2(a.x, a.y), a2[r], x);
-                  }
-                  x = f2_mul(f2_fma(x, f2(2.0f, 2.0f), z2[r]), inv[r]);
-                  chk = f2_fma(x, 0ull, chk);
-                  *reinterpret_cast<float2*>(dst[r] + 32 * i + 8 * c + 2 * quad) = f2_get(x);
+                  const float2 a = asc[r] != 0.0f ? sum : make_float2(0.0f, 0.0f);
+                  x = f2_mul(f2_fma(f2_fma(f2(a.x, a.y), a2[r], x), f2(2.0f, 2.0f), z2[r]), inv[r]);
+                  if (v0[r]) chk = f2_fma(x, 0ull, chk);
+                  sum = f2_get(x);
                 }
             }
+            // the rows leave from where their sums were, one bulk copy each (written from the
+            // registers, 32 bytes of eight rows at a time, a unit's rows took 10000 cycles)
+            tc::fence_async_smem();
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (quad == 0 && v0[r])
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], 512;" ::"l"(dst[r]),
+                             "r"(smem_addr(&sums(0, r)))
+                             : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             const float2 ck = f2_get(chk);
             if (ck.x != 0.0f || ck.y != 0.0f) flag_error(p.err, KVQ_DEV_ERR_RANGE);
 #pragma unroll
@@ -1030,7 +1040,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               }
           }
         }
-        if (done) break;
+        if (done) {
+          asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+          break;
+        }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           M[r] = -INFINITY;
@@ -1054,25 +1067,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           // masked places, whatever they hold, become -inf: tokens that are not there or not seen
           const int ng = raw ? 0 : (wk.s.np - wk.k * PPT) << p.gpp_log2;  // groups that hold tokens
           if (quad >= ng) zr[0] = zr[1] = 0u;
+          uint32_t mine[2] = {0u, 0u};  // bits of the tokens of group `quad` that the rows see
+          if (raw) {
+            const int xw = 128 * (wk.k - wk.s.ntp) + 32 * quad, in_window = wk.s.rl - xw;
+            const int d = xw - wk.s.rl, wd = d >> 5;  // d: first drafted token of the group
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t* mask = p.mask + (size_t(wk.b) * p.T + ((128 * wk.r + row + 8 * r) >> p.gqa_log2)) * p.W;
+              auto word = [&](int j) {  // of the row's mask, without what is behind draft_len
+                const int left = wk.s.dl - 32 * j;
+                return valid[r] && j >= 0 && left > 0 ? __ldcg(mask + j) & (left >= 32 ? kFull : (1u << left) - 1u) : 0u;
+              };
+              const uint32_t drafted = d > -32 ? __funnelshift_r(word(wd), word(wd + 1), uint32_t(d) & 31u) : 0u;
+              mine[r] = in_window >= 32 ? kFull : drafted | (in_window > 0 ? (1u << in_window) - 1u : 0u);
+            }
+          }
 #pragma unroll 1
           for (int g = ng; g < 4; ++g) {
-            uint32_t x[16], see[2] = {0u, 0u};
-            if (raw) {
-              // bits of the 32 tokens from token xw of the raw sequence on, the lane's first lowest
-              const int xw = 128 * (wk.k - wk.s.ntp) + 32 * g, in_window = wk.s.rl - xw;
-              if (in_window >= 32) continue;
-              const int d = xw - wk.s.rl, wd = d >> 5;  // d: first drafted token of the word
-              const uint32_t v = in_window > 0 ? (1u << in_window) - 1u : 0u;
+            uint32_t x[16], see[2];
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const uint32_t* mask = p.mask + (size_t(wk.b) * p.T + ((128 * wk.r + row + 8 * r) >> p.gqa_log2)) * p.W;
-                auto word = [&](int j) {  // of the row's mask, without what is behind draft_len
-                  const int left = wk.s.dl - 32 * j;
-                  return valid[r] && j >= 0 && left > 0 ? __ldcg(mask + j) & (left >= 32 ? kFull : (1u << left) - 1u) : 0u;
-                };
-                see[r] = (v | __funnelshift_r(word(wd), word(wd + 1), uint32_t(d) & 31u)) >> (2 * quad);
-              }
-            }
+            for (int r = 0; r < 2; ++r) see[r] = __shfl_sync(kFull, mine[r], (lane & ~3) + g);
+            if (__all_sync(kFull, (see[0] & see[1]) == kFull)) continue;
+            see[0] >>= 2 * quad;  // the lane's first token lowest
+            see[1] >>= 2 * quad;
             ld32(tS + 32 * g, x);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -1141,6 +1158,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           zs[r] += z.x + z.y;
         }
         const bool flush = run > 0 && run % kFlush == 0;
+        if (flush && run == kFlush) {  // the rows of the unit before have left
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+        }
         if (flush || (run > 0 && __any_sync(kFull, alpha[0] != 1.0f || alpha[1] != 1.0f))) {
           // O into the sums, to start anew with this tile; or only to the new reference
           wait_pv(it - 1);
