@@ -37,6 +37,7 @@
 // p * sV is one register that movmatrix turns into the B fragment of the PV product.
 #pragma once
 #include <algorithm>
+#include <type_traits>
 
 #include "kvq_internal.cuh"
 
@@ -457,11 +458,12 @@ __device__ __forceinline__ void page_group(const uint8_t* rec, int grp, const La
 
 // One piece of n <= 16 residual tokens staged in shared memory as K rows then V rows
 // (272-byte rows; rows n..15 hold zeros).  The PV operand carries 0.5 * p so
-// that the accumulator stays in the units of the code products.
+// that the accumulator stays in the units of the code products.  Two bf16 parts of it hold 17
+// bits; `fine` adds a third (sparse mode, where the window is a large share of the tokens).
 template <typename T, int GQA>
 __device__ __forceinline__ void residual_piece(const uint8_t* Kr, const uint8_t* Vr, int n, const uint16_t* qs,
                                                WarpState<(GQA > 4 ? 2 : 1)>& st, int lane, float c_log2,
-                                               int32_t* err) {
+                                               int32_t* err, bool fine) {
   constexpr int NT = GQA > 4 ? 2 : 1;
   const int g = lane >> 2, li = lane >> 3, lr = lane & 7;
   const bool lo = g & 1;  // lo-part columns get no query: the raw query is exact
@@ -491,21 +493,38 @@ __device__ __forceinline__ void residual_piece(const uint8_t* Kr, const uint8_t*
     for (int r = 0; r < 2; ++r)
       L[0][nt][r] = (g + 8 * r) < n ? (acc[nt][2 * r] + acc[nt][2 * r + 1]) * c_log2 : -INFINITY;
   softmax_step<NT, 1>(st, L, err);
+  constexpr bool kThird = std::is_same<T, __nv_bfloat16>::value;
   uint32_t pb[NT][2];
+  float rest[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const float pr = ex2(L[0][nt][r] - st.m[nt]);
       st.l[nt] += pr;
-      pb[nt][r] = movmatrix_trans(hilo(0.5f * pr * st.fsc, T()));
+      const float x = 0.5f * pr * st.fsc;
+      const uint32_t hl = hilo(x, T());
+      if constexpr (kThird) {
+        const float2 f = t2_to_float2(hl, T());
+        rest[nt][r] = x - f.x - f.y;
+      }
+      pb[nt][r] = movmatrix_trans(hl);
     }
+#pragma unroll 1
+  for (int part = 0; part < (kThird && fine ? 2 : 1); ++part) {
 #pragma unroll
-  for (int mc = 0; mc < 8; ++mc) {
-    uint32_t a[4];
-    ldmatrix_x4_trans(a, smem_addr(Vr + (lr + 8 * (li >> 1)) * kResRowBytes + (16 * mc + 8 * (li & 1)) * 2));
+    for (int mc = 0; mc < 8; ++mc) {
+      uint32_t a[4];
+      ldmatrix_x4_trans(a, smem_addr(Vr + (lr + 8 * (li >> 1)) * kResRowBytes + (16 * mc + 8 * (li & 1)) * 2));
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mma_16816(st.o[mc][nt], a, pb[nt][0], pb[nt][1], T());
+      for (int nt = 0; nt < NT; ++nt) mma_16816(st.o[mc][nt], a, pb[nt][0], pb[nt][1], T());
+    }
+    if constexpr (kThird) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) pb[nt][r] = movmatrix_trans(hilo(rest[nt][r], T()));
+    }
   }
 }
 
@@ -1237,7 +1256,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
             const int pw = (32 * warp) / P, grp = ((32 * warp) % P) / 32;
             if (pw < n) page_group<T, GQA, KB, P>(sb + pw * R::record, grp, lq, qs, st, lane, p.err);
           } else if (int(d.w >> 16) % 4 == warp) {
-            residual_piece<T, GQA>(sb, sb + kPieceTokens * kResRowBytes, n, qs, st, lane, p.c_log2, p.err);
+            residual_piece<T, GQA>(sb, sb + kPieceTokens * kResRowBytes, n, qs, st, lane, p.c_log2, p.err, p.sel != nullptr);
           }
         }
         // release the stage; the last warp to release it refills it with item xi + kStages
