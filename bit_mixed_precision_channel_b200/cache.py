@@ -12,6 +12,8 @@ whole page, then attend over pages + window.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import binding as kb
@@ -39,6 +41,12 @@ class PagedKVCache:
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.new_page = torch.full((batch,), -1, dtype=torch.int32, device=self.device)
         self.counters = torch.zeros(batch, dtype=torch.int32, device=self.device)  # append_flush arrivals
+        # speculative decoding: the last choice of pages, the accepted lengths, the tree's scratch
+        self.sel = None
+        self.n_sel = torch.zeros(batch, dtype=torch.int32, device=self.device)
+        self.n_path = torch.zeros(batch, dtype=torch.int32, device=self.device)
+        self.taken = torch.zeros(batch, dtype=torch.int32, device=self.device)
+        self.tree_workspace = None
         # host mirrors used to hand out pages
         order = list(range(pool_pages)) if page_order is None else [int(x) for x in page_order]
         if sorted(order) != list(range(pool_pages)):
@@ -153,6 +161,73 @@ class PagedKVCache:
             self.flush(stream)
         self.attend(q, out, sm_scale, stream)
         self.commit_host(flushing)
+
+    # ---------------------------------------------------------------- speculative decoding
+    # A round drafts tokens with `attend_few` (or any other drafter), attends from the drafted
+    # tree to the whole cache with `verify`, and keeps what was accepted with `accept`.  The
+    # drafted tokens' keys and values stay outside the cache until then.
+
+    def select(self, q, n_select: int, n_first: int = 1, n_recent: int = 1, stream=None):
+        """Chooses the n_select pages of every (sequence, KV head) whose stored key ranges
+        allow q the largest logits (the first n_first and the last n_recent always): fills
+        and returns self.sel [B][Hkv][n_select] and self.n_sel [B].  A choice stays valid
+        while pages are only appended."""
+        if self.sel is None or self.sel.shape[2] != n_select:
+            self.sel = torch.empty(self.batch, self.cfg.num_kv_heads, n_select, dtype=torch.int32, device=self.device)
+        kb.select_pages(self.cfg, self.pool, q, self.page_table, self.num_pages, self.sel, self.n_sel, n_first, n_recent,
+                        self.err, stream)
+        return self.sel, self.n_sel
+
+    def attend_few(self, q, out, sm_scale=None, stream=None):
+        """Decode attention over the pages of the last `select` and the window."""
+        if self.sel is None:
+            raise RuntimeError("attend_few needs a choice of pages: call select first")
+        kb.decode_attention_sparse(self.cfg, self.pool, q, self.page_table, self.num_pages, self.sel, self.n_sel,
+                                   self.res_k, self.res_v, self.res_len, out, self.workspace, sm_scale, self.err, stream)
+
+    def verify(self, q, k_draft, v_draft, mask, draft_len, out, sm_scale=None, stream=None):
+        """Attention from the drafted tokens (q [B][T][Hq][D]) to the whole cache, the window and
+        the drafted tokens their mask names; see tree_attention.  The cache is not changed."""
+        need = kb.tree_workspace_bytes(self.cfg, self.batch, q.shape[1])
+        if self.tree_workspace is None or self.tree_workspace.numel() < need:
+            self.tree_workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        kb.tree_attention(self.cfg, self.pool, q, self.page_table, self.num_pages, self.res_k, self.res_v, self.res_len,
+                          k_draft, v_draft, mask, draft_len, out, self.tree_workspace, sm_scale, self.err, stream)
+
+    def accept(self, k_draft, v_draft, path, n_path, stream=None):
+        """Appends the accepted tokens path[b][:n_path[b]] (path: int32 [B][T] on the device,
+        n_path: integers on the host) of k_draft, v_draft [B][T][Hkv][D] to every sequence and
+        flushes the windows they fill.  Nothing is changed if pages run out."""
+        P, T = self.cfg.page_tokens, path.shape[1]
+        left = [int(n) for n in n_path]
+        if len(left) != self.batch or any(n < 0 or n > T for n in left):
+            raise ValueError(f"n_path: {self.batch} lengths from 0 to {T}, not {left}")
+        fills = [(r + n) // P for r, n in zip(self.host_res_len, left)]
+        if any(len(h) + f > self.max_pages for h, f in zip(self.host_pages, fills)):
+            raise RuntimeError("page table full")
+        if sum(fills) > len(self.free):
+            raise RuntimeError("page pool exhausted")
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            self.n_path.copy_(torch.tensor(left, dtype=torch.int32))
+            self.taken.zero_()
+            while True:
+                kb.append_path(self.cfg, k_draft, v_draft, path, self.n_path, self.taken, self.res_k, self.res_v,
+                               self.res_len, self.err, stream)
+                ids = [-1] * self.batch
+                for b in range(self.batch):
+                    t = min(left[b], P - self.host_res_len[b])
+                    left[b] -= t
+                    self.host_res_len[b] += t
+                    if self.host_res_len[b] == P:
+                        ids[b] = self.take_pages(1)[0]
+                        self.host_pages[b].append(ids[b])
+                        self.host_res_len[b] = 0
+                if any(i >= 0 for i in ids):
+                    self.new_page.copy_(torch.tensor(ids, dtype=torch.int32))
+                    self.host_new_page = ids
+                    self.flush(stream)
+                if not any(left):
+                    break
 
     def record(self, page: int, head: int) -> torch.Tensor:
         """Bytes of record (page, head) (a view into the pool)."""

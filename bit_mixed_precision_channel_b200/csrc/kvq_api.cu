@@ -425,7 +425,7 @@ kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int64_t poo
   p.sel = sel;
   p.n_sel = n_sel;
   p.err = err;
-  return cuda_status(launch_select_pages(p, cfg->page_tokens, cfg->dtype, stream));
+  return cuda_status(launch_select_pages(p, cfg->page_tokens, cfg->dtype, sm_count(), stream));
 }
 
 size_t kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n_draft) {

@@ -400,7 +400,7 @@ cudaError_t launch_append(const void* k_new, const void* v_new, void* res_k, voi
 cudaError_t launch_append_path(const void* k_draft, const void* v_draft, const int32_t* path, const int32_t* n_path,
                                int32_t* taken, int T, void* res_k, void* res_v, int32_t* res_len, int batch, int Hkv,
                                int P, int32_t* err, cudaStream_t stream);
-cudaError_t launch_select_pages(const SelectParams& p, int P, int dtype, cudaStream_t stream);
+cudaError_t launch_select_pages(const SelectParams& p, int P, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_tree(const TreeParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_flush_commit(int32_t* res_len, const int32_t* new_page, int32_t* page_table, int max_pages,
                                 int32_t* num_pages, long long pool_pages, int batch, int P, cudaStream_t stream);

@@ -7,10 +7,12 @@
 //   pos_c = sum_h max(q_hc, 0), neg_c = sum_h min(q_hc, 0) over the query heads of the kv head.
 // The score of a page is the largest such bound over its 32-token groups.
 //
-// One cluster of 8 CTAs per (sequence, kv head): each CTA scores an eighth of the pages (a
-// warp per page; the record's scales and zeros, 2 KB of its 12, are all it reads), the keys
-// stay in shared memory, and the choice is made there, so there is one launch and no
-// workspace.  Up to 256 pages, CTA 0 gathers the keys and ranks them by counting (a thread
+// One cluster of up to 8 CTAs per (sequence, kv head): each CTA scores its share of the pages
+// (a warp per page, the next page's scales and zeros loading meanwhile; they, 2 KB of the
+// record's 12, are all it reads), the keys stay in shared memory, and the choice is made
+// there, so there is one launch and no workspace.  The cluster is as large as keeps all CTAs
+// resident at once: alone on the GPU 8 units finish soonest on 64 CTAs, and 512 units on
+// 1024 (fewer pages a warp would only repeat the CTAs' set-up).  Up to 256 pages, CTA 0 gathers the keys and ranks them by counting (a thread
 // per page); above, the cluster runs a radix select, 8 bits a pass, summing the CTAs'
 // histograms through distributed shared memory.
 //
@@ -26,7 +28,6 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int kSelThreads = 256;
-constexpr int kSelCluster = 8;
 constexpr int kSelRankMax = kSelThreads;  // pages ranked by counting
 
 // A 16-bit value as a double times 2^-kBias: its exponent and mantissa bits moved into
@@ -57,7 +58,7 @@ struct SelShared {
   double wa[kHeadDim];   // 3 pos at the stored position of the channel
   double wz[kHeadDim];   // pos + neg, the same order
   double wb[kHeadDim];   // 3 pos in channel order, for the boosted rows
-  uint32_t hist[2][256];
+  __align__(16) uint32_t hist[2][256];
   uint32_t cnt[2];       // own pages above / at the threshold
   uint32_t warp_sum[2][kSelThreads / 32];
   int bin, rest;
@@ -90,50 +91,68 @@ __device__ __forceinline__ void scan2(SelShared& sh, bool a, bool b, int tid, ui
 
 }  // namespace
 
-// Score of one page (all lanes return it): GP groups of 32 tokens.  Lane i holds the stored
-// positions 4i .. 4i + 3 of the scales and zeros, and the boosted rows i, i + 32, ...
-template <typename T, int GP>
-__device__ __forceinline__ double page_score(const uint8_t* rec, const SelectParams& p, const double (&wa)[4],
-                                             const double (&wz)[4], const double* wb, int lane) {
+// What the score of a page needs of its record, GP groups of 32 tokens.  Lane i holds the
+// stored positions 4i .. 4i + 3 of the scales and zeros, and the boosted rows i, i + 32, ...
+template <int GP, int JN>
+struct PageMeta {
   uint2 sc[GP], ze[GP];
+  uint32_t sb[JN > 0 ? JN : 1][GP];
+  uint32_t idx[JN > 0 ? JN : 1];
+};
+
+template <int GP, int JN>
+__device__ __forceinline__ void page_load(const uint8_t* rec, const SelectParams& p, PageMeta<GP, JN>& m, int lane) {
 #pragma unroll
   for (int g = 0; g < GP; ++g) {
-    sc[g] = __ldcg(reinterpret_cast<const uint2*>(rec + p.L.k_scale + g * 256) + lane);
-    ze[g] = __ldcg(reinterpret_cast<const uint2*>(rec + p.L.k_zero + g * 256) + lane);
+    m.sc[g] = __ldcg(reinterpret_cast<const uint2*>(rec + p.L.k_scale + g * 256) + lane);
+    m.ze[g] = __ldcg(reinterpret_cast<const uint2*>(rec + p.L.k_zero + g * 256) + lane);
   }
-  double x[GP];
 #pragma unroll
-  for (int g = 0; g < GP; ++g) x[g] = 0.0;
-  for (int j = lane; j < p.k; j += 32) {
-    const double w = wb[__ldcg(rec + p.L.boost_idx + j) & 127];
+  for (int i = 0; i < JN; ++i) {
+    const int j = lane + 32 * i;
+    const bool in = j < p.k;
+    m.idx[i] = in ? __ldcg(rec + p.L.boost_idx + j) : 0u;
 #pragma unroll
     for (int g = 0; g < GP; ++g)
-      x[g] = fma(biased(__ldcg(reinterpret_cast<const uint16_t*>(rec + p.L.kb_scale) + g * p.k + j), T()), w, x[g]);
+      m.sb[i][g] = in ? __ldcg(reinterpret_cast<const uint16_t*>(rec + p.L.kb_scale) + g * p.k + j) : 0u;
   }
+}
+
+// Score of one page (all lanes return it).
+template <typename T, int GP, int JN>
+__device__ __forceinline__ double page_score(const PageMeta<GP, JN>& m, const double (&wa)[4], const double (&wz)[4],
+                                             const double* wb, int lane) {
+  double x[GP];
 #pragma unroll
   for (int g = 0; g < GP; ++g) {
-    x[g] = fma(biased(sc[g].x & 0xffffu, T()), wa[0], x[g]);
-    x[g] = fma(biased(sc[g].x >> 16, T()), wa[1], x[g]);
-    x[g] = fma(biased(sc[g].y & 0xffffu, T()), wa[2], x[g]);
-    x[g] = fma(biased(sc[g].y >> 16, T()), wa[3], x[g]);
-    x[g] = fma(biased(ze[g].x & 0xffffu, T()), wz[0], x[g]);
-    x[g] = fma(biased(ze[g].x >> 16, T()), wz[1], x[g]);
-    x[g] = fma(biased(ze[g].y & 0xffffu, T()), wz[2], x[g]);
-    x[g] = fma(biased(ze[g].y >> 16, T()), wz[3], x[g]);
+    x[g] = biased(m.sc[g].x & 0xffffu, T()) * wa[0];
+    x[g] = fma(biased(m.sc[g].x >> 16, T()), wa[1], x[g]);
+    x[g] = fma(biased(m.sc[g].y & 0xffffu, T()), wa[2], x[g]);
+    x[g] = fma(biased(m.sc[g].y >> 16, T()), wa[3], x[g]);
+    x[g] = fma(biased(m.ze[g].x & 0xffffu, T()), wz[0], x[g]);
+    x[g] = fma(biased(m.ze[g].x >> 16, T()), wz[1], x[g]);
+    x[g] = fma(biased(m.ze[g].y & 0xffffu, T()), wz[2], x[g]);
+    x[g] = fma(biased(m.ze[g].y >> 16, T()), wz[3], x[g]);
+  }
+#pragma unroll
+  for (int i = 0; i < JN; ++i) {
+    const double w = wb[m.idx[i] & 127];
+#pragma unroll
+    for (int g = 0; g < GP; ++g) x[g] = fma(biased(m.sb[i][g], T()), w, x[g]);
   }
   // the lanes' parts of the GP sums: halve the number of sums a lane carries while there
   // are several, so that four groups take 6 exchanges instead of 20
-  int m = 16;
+  int h = 16;
 #pragma unroll
-  for (int n = GP; n > 1; n >>= 1, m >>= 1) {
-    const bool up = lane & m;
+  for (int n = GP; n > 1; n >>= 1, h >>= 1) {
+    const bool up = lane & h;
 #pragma unroll
     for (int i = 0; i < n / 2; ++i) {
       const double keep = up ? x[i + n / 2] : x[i], give = up ? x[i] : x[i + n / 2];
-      x[i] = keep + shfl_xor_d(give, m);
+      x[i] = keep + shfl_xor_d(give, h);
     }
   }
-  for (; m > 0; m >>= 1) x[0] += shfl_xor_d(x[0], m);
+  for (; h > 0; h >>= 1) x[0] += shfl_xor_d(x[0], h);
   double best = x[0];
 #pragma unroll
   for (int n = GP, b = 16; n > 1; n >>= 1, b >>= 1) {
@@ -143,13 +162,13 @@ __device__ __forceinline__ double page_score(const uint8_t* rec, const SelectPar
   return best;
 }
 
-template <typename T, int GP>
+template <typename T, int GP, int JN>
 __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_constant__ SelectParams p) {
   extern __shared__ __align__(16) unsigned long long keys[];  // own pages' keys; in CTA 0 room for kSelRankMax
   __shared__ SelShared sh;
   cg::cluster_group cl = cg::this_cluster();
-  const int rank = int(cl.block_rank());
-  const int u = blockIdx.x / kSelCluster, b = u / p.Hkv, h = u - b * p.Hkv;
+  const int rank = int(cl.block_rank()), ctas = int(cl.num_blocks());
+  const int u = blockIdx.x / ctas, b = u / p.Hkv, h = u - b * p.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
@@ -194,17 +213,25 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
   }
 
   // ---- scores of the own pages [s0, s1); pages that are kept anyway get the largest key
-  const int per = (np + kSelCluster - 1) / kSelCluster;
+  const int per = (np + ctas - 1) / ctas;
   const int s0 = min(np, rank * per), s1 = min(np, s0 + per);
+  // (a page that is kept anyway is read like the others: no branch around the loads)
+  auto load = [&](int s, PageMeta<GP, JN>& m) {
+    int id = __ldcg(p.page_table + size_t(b) * p.max_pages + s);
+    if (id < 0 || id >= p.pool_pages) {
+      if (lane == 0 && s >= p.n_first && s < np - p.n_recent) flag_error(p.err, KVQ_DEV_ERR_PAGE_RANGE);
+      id = 0;
+    }
+    page_load<GP, JN>(p.pool + (size_t(id) * p.Hkv + h) * p.L.record, p, m, lane);
+  };
+  PageMeta<GP, JN> m;
+  if (s0 + warp < s1) load(s0 + warp, m);
   for (int s = s0 + warp; s < s1; s += kSelThreads / 32) {
+    const PageMeta<GP, JN> now = m;
+    if (s + kSelThreads / 32 < s1) load(s + kSelThreads / 32, m);
     unsigned long long key = ~0ull;
     if (s >= p.n_first && s < np - p.n_recent) {
-      int id = __ldcg(p.page_table + size_t(b) * p.max_pages + s);
-      if (id < 0 || id >= p.pool_pages) {
-        if (lane == 0) flag_error(p.err, KVQ_DEV_ERR_PAGE_RANGE);
-        id = 0;
-      }
-      const double x = page_score<T, GP>(p.pool + (size_t(id) * p.Hkv + h) * p.L.record, p, wa, wz, sh.wb, lane);
+      const double x = page_score<T, GP, JN>(now, wa, wz, sh.wb, lane);
       if (x != x && lane == 0) flag_error(p.err, KVQ_DEV_ERR_RANGE);
       key = order_key(x);
     }
@@ -217,14 +244,29 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
     if (rank == 0 && tid < np) mine = cl.map_shared_rank(keys, tid / per)[tid % per];
     cl.sync();  // the other CTAs' shared memory is no longer read
     if (rank != 0) return;
+    // pages before this one: by the upper halves of the keys, four at a time; where two of
+    // them are equal, by the keys and then the slots
+    uint32_t* upper = sh.hist[0];
+    const uint32_t up = uint32_t(mine >> 32);
+    upper[tid] = up;
     if (tid < np) keys[tid] = mine;
     __syncthreads();
     int before = 0;
-    if (tid < np)
-      for (int j = 0; j < np; ++j) {
-        const unsigned long long o = keys[j];
-        before += (o > mine || (o == mine && j < tid)) ? 1 : 0;
+    if (tid < np) {
+      int same = 0;
+      for (int j = 0; j < np; j += 4) {
+        const uint4 o = lds128(upper + j);  // behind the last page: 0
+        before += (o.x > up) + (o.y > up) + (o.z > up) + (o.w > up);
+        same += (o.x == up) + (o.y == up) + (o.z == up) + (o.w == up);
       }
+      if (same > 1) {
+        before = 0;
+        for (int j = 0; j < np; ++j) {
+          const unsigned long long o = keys[j];
+          before += (o > mine || (o == mine && j < tid)) ? 1 : 0;
+        }
+      }
+    }
     const bool keep = tid < np && before < n;
     uint32_t at, none, total, zero;
     scan2(sh, keep, false, tid, at, none, total, zero);
@@ -247,7 +289,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
     }
     cl.sync();
     uint32_t c = 0;
-    for (int r = 0; r < kSelCluster; ++r) c += cl.map_shared_rank(hist, r)[tid];
+    for (int r = 0; r < ctas; ++r) c += cl.map_shared_rank(hist, r)[tid];
     // bins from the top: thread t holds bin t; pages in higher bins
     uint32_t incl = c;
 #pragma unroll
@@ -312,15 +354,21 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
   }
 }
 
-template <typename T, int GP>
-static cudaError_t launch_select_t(const SelectParams& p, cudaStream_t stream) {
-  const size_t own = (size_t(p.max_pages) + kSelCluster - 1) / kSelCluster;
+template <typename T, int GP, int JN>
+static cudaError_t launch_select_t(const SelectParams& p, int sms, cudaStream_t stream) {
+  // 8 CTAs an SM (512 units of 30 to 250 pages on 1, 2, 4, 8 CTAs each: 57, 51, 59, 72 us); a
+  // CTA's keys have to fit its shared memory
+  const long long units = (long long)p.batch * p.Hkv;
+  int ctas = 8;
+  while (ctas > 1 && units * ctas > 8ll * sms) ctas /= 2;
+  while (ctas < 8 && (long long)p.max_pages > 1024ll * ctas) ctas *= 2;
+  const size_t own = (size_t(p.max_pages) + ctas - 1) / ctas;
   const size_t smem = (own > kSelRankMax ? own : size_t(kSelRankMax)) * sizeof(unsigned long long);
   static int seen[64];
-  cudaError_t e = ensure_dynamic_smem(select_pages_kernel<T, GP>, int(smem), seen);
+  cudaError_t e = ensure_dynamic_smem(select_pages_kernel<T, GP, JN>, int(smem), seen);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.batch) * unsigned(p.Hkv) * kSelCluster);
+  cfg.gridDim = dim3(unsigned(units) * unsigned(ctas));
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -328,26 +376,39 @@ static cudaError_t launch_select_t(const SelectParams& p, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kSelCluster;
+  attr[1].val.clusterDim.x = ctas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_pages_kernel<T, GP>, p);
+  return cudaLaunchKernelEx(&cfg, select_pages_kernel<T, GP, JN>, p);
 }
 
-template <typename T>
-static cudaError_t launch_select_p(const SelectParams& p, int P, cudaStream_t stream) {
-  switch (P) {
-    case 32: return launch_select_t<T, 1>(p, stream);
-    case 64: return launch_select_t<T, 2>(p, stream);
-    case 128: return launch_select_t<T, 4>(p, stream);
+template <typename T, int GP>
+static cudaError_t launch_select_k(const SelectParams& p, int sms, cudaStream_t stream) {
+  switch (p.k) {
+    case 0: return launch_select_t<T, GP, 0>(p, sms, stream);
+    case 16:
+    case 32: return launch_select_t<T, GP, 1>(p, sms, stream);
+    case 64: return launch_select_t<T, GP, 2>(p, sms, stream);
+    case 128: return launch_select_t<T, GP, 4>(p, sms, stream);
   }
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_select_pages(const SelectParams& p, int P, int dtype, cudaStream_t stream) {
-  return dtype == KVQ_BF16 ? launch_select_p<__nv_bfloat16>(p, P, stream) : launch_select_p<__half>(p, P, stream);
+template <typename T>
+static cudaError_t launch_select_p(const SelectParams& p, int P, int sms, cudaStream_t stream) {
+  switch (P) {
+    case 32: return launch_select_k<T, 1>(p, sms, stream);
+    case 64: return launch_select_k<T, 2>(p, sms, stream);
+    case 128: return launch_select_k<T, 4>(p, sms, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_select_pages(const SelectParams& p, int P, int dtype, int sms, cudaStream_t stream) {
+  return dtype == KVQ_BF16 ? launch_select_p<__nv_bfloat16>(p, P, sms, stream)
+                           : launch_select_p<__half>(p, P, sms, stream);
 }
 
 }  // namespace kvq
