@@ -190,7 +190,7 @@ class PagedKVCache:
         the drafted tokens their mask names; see tree_attention.  The cache is not changed."""
         need = kb.tree_workspace_bytes(self.cfg, self.batch, q.shape[1])
         if self.tree_workspace is None or self.tree_workspace.numel() < need:
-            self.tree_workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            self.tree_workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
         kb.tree_attention(self.cfg, self.pool, q, self.page_table, self.num_pages, self.res_k, self.res_v, self.res_len,
                           k_draft, v_draft, mask, draft_len, out, self.tree_workspace, sm_scale, self.err, stream)
 

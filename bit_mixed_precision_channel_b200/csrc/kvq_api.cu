@@ -428,10 +428,38 @@ kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int64_t poo
   return cuda_status(launch_select_pages(p, cfg->page_tokens, cfg->dtype, sm_count(), stream));
 }
 
+// Tree attention with at most 8 rows (drafted token, query head) of a kv head runs on the
+// decode kernel, whose products take their rows eight at a time: the number it is built for,
+// or 0 where the rows go to the tensor-memory kernel.  Measured on 16 x 4096 tokens, 32/8
+// heads: 4 rows XX us here, YY us there; 8 rows XX and YY us.
+static int draft_rows(const kvq_config* cfg, int n_draft) {
+  const long long rows = (long long)n_draft * (cfg->num_q_heads / cfg->num_kv_heads);
+  return rows > 8 ? 0 : rows > 4 ? 8 : rows > 2 ? 4 : int(rows);
+}
+// The configuration whose query heads are those rows.
+static kvq_config draft_config(const kvq_config* cfg, int rows) {
+  kvq_config c = *cfg;
+  c.num_q_heads = c.num_kv_heads * rows;
+  return c;
+}
+
+// The workspace starts with the arrival counters of the few-row form, at one place for every
+// shape, so that calls of any shapes can take turns in it; more units than it holds have
+// theirs behind the parts, cleared by each call.
+constexpr size_t kTreeCounters = 16384;
+
 size_t kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n_draft) {
   if (kvq_check_config(cfg) != KVQ_OK || batch < 0 || n_draft < 1 || n_draft > KVQ_MAX_DRAFT) return 0;
-  // two parts of 128 rows and one list entry per CTA
-  return size_t(sm_count()) * (2 * 128 * (kHeadDim + 4) * sizeof(float) + sizeof(int4));
+  size_t bytes = kTreeCounters * sizeof(uint32_t);
+  if (const int rows = draft_rows(cfg, n_draft)) {
+    const kvq_config c = draft_config(cfg, rows);
+    const Plan pl = decode_plan(&c, batch);
+    bytes += pl.part_bytes + (size_t(batch) * cfg->num_kv_heads > kTreeCounters ? pl.cnt_bytes : 0);
+  } else {
+    // two parts of 128 rows and one list entry per CTA
+    bytes += size_t(sm_count()) * (2 * 128 * (kHeadDim + 4) * sizeof(float) + sizeof(int4));
+  }
+  return bytes;
 }
 
 kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
@@ -454,6 +482,34 @@ kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t p
           (((long long)max_pages * cfg->page_tokens + 127) / 128 + 2) >= (1ll << 31))
     return KVQ_ERR_INVALID_ARG;
   if (workspace_bytes < kvq_tree_workspace_bytes(cfg, batch, n_draft)) return KVQ_ERR_CAPACITY;
+  const int gqa_log2 = gq == 8 ? 3 : gq == 4 ? 2 : gq == 2 ? 1 : 0;
+  if (const int rows = draft_rows(cfg, n_draft)) {
+    // the work line counts the drafted tokens with the window's
+    if ((long long)batch * cfg->num_kv_heads *
+            ((long long)max_pages * (cfg->page_tokens / 32) +
+             (long long)kDecodePieceWeight * ((cfg->page_tokens + n_draft + 15) / 16) + kDecodeMergeWeight) >= (1ll << 31))
+      return KVQ_ERR_INVALID_ARG;
+    const kvq_config c = draft_config(cfg, rows);
+    const Plan pl = decode_plan(&c, batch);
+    uint32_t* counters = static_cast<uint32_t*>(workspace);
+    DecodeParams p = decode_params(&c, pool, pool_pages, q, batch, res_k, res_v, res_len, sm_scale, out,
+                                   counters + kTreeCounters, pl, err);
+    if (size_t(batch) * cfg->num_kv_heads <= kTreeCounters)
+      p.cnt = counters;
+    else if (cudaMemsetAsync(p.cnt, 0, pl.cnt_bytes, stream) != cudaSuccess)
+      return KVQ_ERR_CUDA;
+    p.Hq = cfg->num_q_heads;
+    p.page_table = page_table;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.k_draft = static_cast<const uint16_t*>(k_draft);
+    p.v_draft = static_cast<const uint16_t*>(v_draft);
+    p.mask = mask;
+    p.draft_len = draft_len;
+    p.T = n_draft;
+    p.gqa_log2 = gqa_log2;
+    return cuda_status(launch_draft(p, rows, cfg->dtype, stream));
+  }
   TreeParams p{};
   p.pool = static_cast<const uint8_t*>(pool);
   p.pool_pages = pool_pages;
@@ -466,7 +522,7 @@ kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t p
   p.max_pages = max_pages;
   p.T = n_draft;
   p.W = (n_draft + 31) / 32;
-  p.gqa_log2 = p.gqa == 8 ? 3 : p.gqa == 4 ? 2 : p.gqa == 2 ? 1 : 0;
+  p.gqa_log2 = gqa_log2;
   p.gpp_log2 = p.P == 128 ? 2 : p.P == 64 ? 1 : 0;
   p.L = make_layout(cfg->page_tokens, cfg->head_dim, cfg->num_boost, cfg->key_group);
   p.q = static_cast<const uint16_t*>(q);
@@ -481,7 +537,7 @@ kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t p
   p.draft_len = draft_len;
   p.c_log2 = sm_scale * 1.4426950408889634f;
   p.out = out;
-  p.part = static_cast<float*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint32_t*>(workspace) + kTreeCounters);
   p.n_ctas = sm_count();
   p.cuts = reinterpret_cast<int4*>(p.part + size_t(p.n_ctas) * 2 * 128 * (kHeadDim + 4));
   p.err = err;

@@ -21,6 +21,15 @@ cudaError_t decode_launch_bf16_g4(const DecodeParams& p, cudaStream_t stream);
 cudaError_t decode_occupancy_bf16_g8(int kb, int P, int* n);
 cudaError_t decode_launch_bf16_g8(const DecodeParams& p, cudaStream_t stream);
 
+cudaError_t draft_launch_f16_g1(const DecodeParams& p, cudaStream_t stream);
+cudaError_t draft_launch_f16_g2(const DecodeParams& p, cudaStream_t stream);
+cudaError_t draft_launch_f16_g4(const DecodeParams& p, cudaStream_t stream);
+cudaError_t draft_launch_f16_g8(const DecodeParams& p, cudaStream_t stream);
+cudaError_t draft_launch_bf16_g1(const DecodeParams& p, cudaStream_t stream);
+cudaError_t draft_launch_bf16_g2(const DecodeParams& p, cudaStream_t stream);
+cudaError_t draft_launch_bf16_g4(const DecodeParams& p, cudaStream_t stream);
+cudaError_t draft_launch_bf16_g8(const DecodeParams& p, cudaStream_t stream);
+
 static cudaError_t decode_occupancy(int gqa, int dtype, int kb, int P, int* n) {
   const bool bf = dtype == KVQ_BF16;
   switch (gqa) {
@@ -64,6 +73,19 @@ cudaError_t launch_decode(const DecodeParams& p, int gqa, int dtype, cudaStream_
     case 2: return bf ? decode_launch_bf16_g2(p, stream) : decode_launch_f16_g2(p, stream);
     case 4: return bf ? decode_launch_bf16_g4(p, stream) : decode_launch_f16_g4(p, stream);
     case 8: return bf ? decode_launch_bf16_g8(p, stream) : decode_launch_f16_g8(p, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// Few rows of tree attention on the decode kernel: `rows` (1, 2, 4 or 8) of each kv head.
+cudaError_t launch_draft(const DecodeParams& p, int rows, int dtype, cudaStream_t stream) {
+  if (p.batch <= 0 || p.n_ctas <= 0) return cudaSuccess;
+  const bool bf = dtype == KVQ_BF16;
+  switch (rows) {
+    case 1: return bf ? draft_launch_bf16_g1(p, stream) : draft_launch_f16_g1(p, stream);
+    case 2: return bf ? draft_launch_bf16_g2(p, stream) : draft_launch_f16_g2(p, stream);
+    case 4: return bf ? draft_launch_bf16_g4(p, stream) : draft_launch_f16_g4(p, stream);
+    case 8: return bf ? draft_launch_bf16_g8(p, stream) : draft_launch_f16_g8(p, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -460,10 +460,13 @@ __device__ __forceinline__ void page_group(const uint8_t* rec, int grp, const La
 // (272-byte rows; rows n..15 hold zeros).  The PV operand carries 0.5 * p so
 // that the accumulator stays in the units of the code products.  Two bf16 parts of it hold 17
 // bits; `fine` adds a third (sparse mode, where the window is a large share of the tokens).
-template <typename T, int GQA>
+// DRAFT: token t of the piece is drafted token t - first when that is not negative, and seen
+// by head hd if bit t - first of mk[hd >> gqa_log2] is set.
+template <typename T, int GQA, bool DRAFT>
 __device__ __forceinline__ void residual_piece(const uint8_t* Kr, const uint8_t* Vr, int n, const uint16_t* qs,
                                                WarpState<(GQA > 4 ? 2 : 1)>& st, int lane, float c_log2,
-                                               int32_t* err, bool fine) {
+                                               int32_t* err, bool fine, const uint32_t* mk, int first,
+                                               int gqa_log2) {
   constexpr int NT = GQA > 4 ? 2 : 1;
   const int g = lane >> 2, li = lane >> 3, lr = lane & 7;
   const bool lo = g & 1;  // lo-part columns get no query: the raw query is exact
@@ -492,6 +495,17 @@ __device__ __forceinline__ void residual_piece(const uint8_t* Kr, const uint8_t*
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       L[0][nt][r] = (g + 8 * r) < n ? (acc[nt][2 * r] + acc[nt][2 * r + 1]) * c_log2 : -INFINITY;
+  if constexpr (DRAFT) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint32_t see = mk[((lane & 3) + 4 * nt) >> gqa_log2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int d = g + 8 * r - first;
+        if (d >= 0 && !((see >> (d & 31)) & 1u)) L[0][nt][r] = -INFINITY;
+      }
+    }
+  }
   softmax_step<NT, 1>(st, L, err);
   constexpr bool kThird = std::is_same<T, __nv_bfloat16>::value;
   uint32_t pb[NT][2];
@@ -500,7 +514,8 @@ __device__ __forceinline__ void residual_piece(const uint8_t* Kr, const uint8_t*
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const float pr = ex2(L[0][nt][r] - st.m[nt]);
+      float pr = ex2(L[0][nt][r] - st.m[nt]);
+      if (DRAFT && L[0][nt][r] == -INFINITY) pr = 0.0f;  // a head that has seen nothing yet has no maximum
       st.l[nt] += pr;
       const float x = 0.5f * pr * st.fsc;
       const uint32_t hl = hilo(x, T());
@@ -557,6 +572,16 @@ __device__ __forceinline__ int seq_weight(const DecodeParams& p, int b, int& np,
     np = 0;
     rl = 0;
     return -1;
+  }
+  if (p.k_draft) {  // drafted tokens follow the window's; without any there is no row
+    const int dl = __ldcg(p.draft_len + b);
+    if (dl < 0 || dl > p.T) {
+      np = 0;
+      rl = 0;
+      return -1;
+    }
+    np = dl > 0 ? np : 0;
+    rl = dl > 0 ? rl + dl : 0;
   }
   const int items = np * (P / 32) + kPieceWeight * ((rl + kPieceTokens - 1) / kPieceTokens);
   return items > 0 ? items + kMergeWeight : 0;
@@ -724,7 +749,7 @@ __device__ __forceinline__ int seq_info(const DecodeParams& p, int b, int b0, co
 // ---------------------------------------------------------------- the kernel
 
 // Shared state of one CTA besides the stages.
-template <int GQA, int P>
+template <int GQA, int P, bool DRAFT>
 struct CtaShared {
   uint64_t full_bar[kStages];  // stage filled (bulk-copy bytes landed)
   int rel[kStages];            // warps that released the stage's current item
@@ -740,13 +765,17 @@ struct CtaShared {
   UnitSpan span[32];
   ItemDesc desc[kSegItems];
   int ids[kSegItems][128 / P];
+  // drafted tokens: of each stage's residual piece the masks and the place of the first one
+  uint32_t mk[DRAFT ? kStages : 1][8];
+  int first[DRAFT ? kStages : 1];
+  int lens[DRAFT ? kSegItems : 1];  // of each item's sequence: window tokens, drafted tokens << 16
   __align__(16) uint16_t q[3][GQA * kHeadDim];  // query heads of the last 3 units
 };
 
 // Lists the next segment of this CTA's items (all threads).  One thread walks the units
 // from sh.cur; then every thread fills one descriptor and loads its page ids.
-template <int GQA, int KB, int P>
-__device__ __forceinline__ void build_segment(const DecodeParams& p, CtaShared<GQA, P>& sh, int hi, const Owners& ow,
+template <int GQA, int KB, int P, bool DRAFT>
+__device__ __forceinline__ void build_segment(const DecodeParams& p, CtaShared<GQA, P, DRAFT>& sh, int hi, const Owners& ow,
                                               int tid, bool one_pass) {
   constexpr int PPC = 128 / P, GPP = P / 32;
   if (tid == 0) {
@@ -822,6 +851,7 @@ __device__ __forceinline__ void build_segment(const DecodeParams& p, CtaShared<G
     d.b = sp.b;
     d.h = sp.h;
     d.io = sp.io;
+    if constexpr (DRAFT) sh.lens[t] = __ldcg(p.res_len + sp.b) | (__ldcg(p.draft_len + sp.b) << 16);
     uint32_t w = uint32_t(sp.qslot) << 11;
     if (sp.first && t == sp.off) w |= kDescFirst;
     if (sp.last && t == sp.off + sp.n - 1) w |= kDescLast;
@@ -856,8 +886,8 @@ __device__ __forceinline__ void build_segment(const DecodeParams& p, CtaShared<G
 // Issues the copies of item x (descriptor slot t of the segment) into stage x % kStages:
 // the page records or residual rows, and the unit's query heads with its first item.
 // All lanes of the calling warp take part.
-template <int GQA, int KB, int P>
-__device__ __forceinline__ void issue_item(const DecodeParams& p, CtaShared<GQA, P>& sh, uint8_t* smem, int x, int t,
+template <int GQA, int KB, int P, bool DRAFT>
+__device__ __forceinline__ void issue_item(const DecodeParams& p, CtaShared<GQA, P, DRAFT>& sh, uint8_t* smem, int x, int t,
                                            uint64_t policy, int lane) {
   using R = Rec<P, KB>;
   using S = Smem<GQA, P, KB>;
@@ -865,7 +895,9 @@ __device__ __forceinline__ void issue_item(const DecodeParams& p, CtaShared<GQA,
   const int st = x % kStages, n = d.w & 0xff;
   const bool res = d.w & kDescRes, first = d.w & kDescFirst;
   uint8_t* sb = smem + st * S::stage;
-  const uint32_t bytes = (res ? 0u : uint32_t(n) * R::payload) + (first ? GQA * 256u : 0u);
+  const int dl = DRAFT ? sh.lens[t] >> 16 : 0;
+  const uint32_t qbytes = DRAFT ? uint32_t(dl) << (8 + p.gqa_log2) : GQA * 256u;
+  const uint32_t bytes = (res ? 0u : uint32_t(n) * R::payload) + (first ? qbytes : 0u);
   if (lane == 0) {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (!res) mbar_arrive_expect_tx(&sh.full_bar[st], bytes);
@@ -896,11 +928,33 @@ __device__ __forceinline__ void issue_item(const DecodeParams& p, CtaShared<GQA,
       kr = p.res_k + ((size_t(d.b) * p.Hkv + d.h) * P + t0) * kHeadDim;
       vr = p.res_v + ((size_t(d.b) * p.Hkv + d.h) * P + t0) * kHeadDim;
     }
+    if constexpr (DRAFT) {
+      // window rows, then drafted rows; drafted tokens that no row sees are left zero, whatever they hold
+      const int rl = sh.lens[t] & 0xffff;
+      uint32_t see = 0u, any = 0u;
+      if (t0 + n > rl) {
+        if (lane < dl) see = __ldcg(p.mask + size_t(d.b) * p.T + lane) & ((1u << dl) - 1u);
+        any = __reduce_or_sync(kFull, see);
+      }
+      if (lane < 8) sh.mk[st][lane] = see;
+      if (lane == 0) sh.first[st] = rl - t0;
+      const uint16_t* kd = p.k_draft + (size_t(d.b) * p.T * p.Hkv + d.h) * kHeadDim;
+      const uint16_t* vd = p.v_draft + (size_t(d.b) * p.T * p.Hkv + d.h) * kHeadDim;
+#pragma unroll 4
+      for (int i = lane; i < 2 * kPieceTokens * 16; i += 32) {
+        const int which = i >> 8, row = (i >> 4) & 15, chunk = i & 15, j = t0 + row - rl;  // j: drafted token
+        const bool in = row < n && (j < 0 || ((any >> (j & 31)) & 1u));
+        const uint16_t* src = j < 0 ? (which ? vr : kr) + row * kHeadDim
+                                    : (which ? vd : kd) + size_t(in ? j : 0) * p.Hkv * kHeadDim;
+        cp_async16(sb + (which * kPieceTokens + row) * kResRowBytes + chunk * 16, src + chunk * 8, in ? 16u : 0u);
+      }
+    } else {
 #pragma unroll 4
     for (int i = lane; i < 2 * kPieceTokens * 16; i += 32) {
       const int which = i >> 8, row = (i >> 4) & 15, chunk = i & 15;
       const uint16_t* src = (which ? vr : kr) + (row < n ? row : 0) * kHeadDim + chunk * 8;
       cp_async16(sb + (which * kPieceTokens + row) * kResRowBytes + chunk * 16, src, row < n ? 16u : 0u);
+    }
     }
     cp_async_arrive(&sh.full_bar[st]);
   }
@@ -910,16 +964,39 @@ __device__ __forceinline__ void issue_item(const DecodeParams& p, CtaShared<GQA,
     if (lane == 0) mbar_arrive_expect_tx(&sh.full_bar[st], bytes);
     __syncwarp();
   }
-  if (first && lane == 31) {
+  if constexpr (DRAFT) {
+    // the heads of drafted token `lane`
+    if (first && lane < dl)
+      bulk_g2s(sh.q[(d.w >> 11) & 3] + ((lane << p.gqa_log2) * kHeadDim),
+               p.q + ((size_t(d.b) * p.T + lane) * p.Hq + (size_t(d.h) << p.gqa_log2)) * kHeadDim, 256u << p.gqa_log2,
+               &sh.full_bar[st], policy);
+  } else if (first && lane == 31) {
     const uint16_t* src = p.q + (size_t(d.b) * p.Hq + size_t(d.h) * GQA) * kHeadDim;
     bulk_g2s(sh.q[(d.w >> 11) & 3], src, GQA * 256u, &sh.full_bar[st], policy);
   }
 }
 
+// Output rows of unit (b, h): head i at out_base + out_row(i), for i < out_rows.  Drafted
+// tokens' heads are (token, query head of the kv head); rows behind draft_len stay as they were.
+template <int GQA, bool DRAFT>
+__device__ __forceinline__ float* out_base(const DecodeParams& p, int b, int h) {
+  if (DRAFT) return p.out + (size_t(b) * p.T * p.Hq + (size_t(h) << p.gqa_log2)) * kHeadDim;
+  return p.out + (size_t(b) * p.Hq + size_t(h) * GQA) * kHeadDim;
+}
+template <bool DRAFT>
+__device__ __forceinline__ int out_row(const DecodeParams& p, int i) {
+  if (DRAFT) return ((i >> p.gqa_log2) * p.Hq + (i & ((1 << p.gqa_log2) - 1))) * kHeadDim;
+  return i * kHeadDim;
+}
+template <int GQA, bool DRAFT>
+__device__ __forceinline__ int out_rows(const DecodeParams& p, int b) {
+  return DRAFT ? __ldcg(p.draft_len + b) << p.gqa_log2 : GQA;
+}
+
 // Merges heads h0 .. h0 + HC - 1 of the nc partial states at pu (log-sum-exp) into outu.
 // One warp; lane i holds channels 4i .. 4i + 3.
 template <int HC, int UNROLL>
-__device__ __forceinline__ void merge_heads(const float* pu, size_t slot, int nc, int h0, float* outu, int lane) {
+__device__ __forceinline__ void merge_heads(const float* pu, size_t slot, int nc, int h0, float* outh, int lane) {
   float Mh[HC], Lh[HC];
   float4 Oh[HC];
 #pragma unroll
@@ -959,7 +1036,7 @@ __device__ __forceinline__ void merge_heads(const float* pu, size_t slot, int nc
 #pragma unroll
   for (int h = 0; h < HC; ++h) {
     const float inv = Lh[h] > 0.0f ? 1.0f / Lh[h] : 0.0f;
-    reinterpret_cast<float4*>(outu + (h0 + h) * kHeadDim)[lane] =
+    reinterpret_cast<float4*>(outh + h * kHeadDim)[lane] =
         make_float4(Oh[h].x * inv, Oh[h].y * inv, Oh[h].z * inv, Oh[h].w * inv);
   }
 }
@@ -968,7 +1045,7 @@ __device__ __forceinline__ void merge_heads(const float* pu, size_t slot, int nc
 // contributors i0..i1, merges their partial states (log-sum-exp) into the output.
 // (Written out rather than through merge_heads: inlined into the item loop, the helper
 // changes the loop's register allocation enough to spill at 128 registers.)
-template <int GQA>
+template <int GQA, bool DRAFT>
 __device__ __forceinline__ void merge_partials(const DecodeParams& p, int u, int i0, int i1, float* outu, int lane) {
   uint32_t arrived = 0;
   if (lane == 0) arrived = atomic_add_acq_rel_gpu(p.cnt + u, 1u);
@@ -1019,7 +1096,8 @@ __device__ __forceinline__ void merge_partials(const DecodeParams& p, int u, int
 #pragma unroll
     for (int h = 0; h < HC; ++h) {
       const float inv = Lh[h] > 0.0f ? 1.0f / Lh[h] : 0.0f;
-      reinterpret_cast<float4*>(outu + (h0 + h) * kHeadDim)[lane] =
+      if (DRAFT && h0 + h >= out_rows<GQA, DRAFT>(p, u / p.Hkv)) continue;
+      reinterpret_cast<float4*>(outu + out_row<DRAFT>(p, h0 + h))[lane] =
           make_float4(Oh[h].x * inv, Oh[h].y * inv, Oh[h].z * inv, Oh[h].w * inv);
     }
   }
@@ -1029,7 +1107,7 @@ __device__ __forceinline__ void merge_partials(const DecodeParams& p, int u, int
 // The same with the whole CTA, for a unit end that is the CTA's last item (all four
 // warps are free): thread 96 counts in; if the CTA is the last contributor, warp w
 // merges heads w, w + 4, ...
-template <int GQA>
+template <int GQA, bool DRAFT>
 __device__ __noinline__ void merge_partials_cta(const DecodeParams& p, int* flag, int u, int i0, int i1, float* outu,
                                                    int warp, int lane) {
   const int nc = i1 - i0 + 1;
@@ -1037,18 +1115,20 @@ __device__ __noinline__ void merge_partials_cta(const DecodeParams& p, int* flag
   named_sync();  // the count (and, through it, the other contributors' partials) is seen by all
   if (*flag != nc - 1) return;
   const float* pu = p.part + (size_t(i0) + u) * GQA * kPartStride;
-  for (int h = warp; h < GQA; h += 4) merge_heads<1, 8>(pu, size_t(GQA) * kPartStride, nc, h, outu, lane);
+  const int rows = out_rows<GQA, DRAFT>(p, u / p.Hkv);
+  for (int h = warp; h < rows; h += 4)
+    merge_heads<1, 8>(pu, size_t(GQA) * kPartStride, nc, h, outu + out_row<DRAFT>(p, h), lane);
   if (warp == 3 && lane == 0) p.cnt[u] = 0u;  // ready for the next launch
 }
 
-template <typename T, int GQA, int KB, int P>
+template <typename T, int GQA, int KB, int P, bool DRAFT>
 __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
     decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int NT = GQA > 4 ? 2 : 1;
   using R = Rec<P, KB>;
   using S = Smem<GQA, P, KB>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ CtaShared<GQA, P> sh;
+  __shared__ CtaShared<GQA, P, DRAFT> sh;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, qd = lane & 3;
   const int cta = range_of_cta(blockIdx.x, p.n_ctas, p.n_sms);
@@ -1069,7 +1149,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
       int np, rl;
       const int w = seq_weight<P>(p, b, np, rl);
       if (w < 0 && cta == 0) flag_error(p.err, KVQ_DEV_ERR_LENGTH);
-      if (w <= 0 && b % p.n_ctas == cta) {  // nothing to attend to: the output is 0
+      if (!DRAFT && w <= 0 && b % p.n_ctas == cta) {  // nothing to attend to: the output is 0
         float4* o = reinterpret_cast<float4*>(p.out + size_t(b) * p.Hq * kHeadDim);
         for (int i = 0; i < p.Hq * kHeadDim / 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
@@ -1104,6 +1184,9 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
   ow.W = W;
   ow.Cs = min(p.n_ctas, max(1, W / 4));
   if (cta >= ow.Cs) return;
+  if constexpr (DRAFT)  // heads that no drafted token fills
+    for (int i = tid; i < 3 * GQA * kHeadDim / 8; i += kDecodeThreads)
+      reinterpret_cast<uint4*>(sh.q)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sh.full_bar[s], 1);
@@ -1190,10 +1273,10 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
   {
     locate(lo);
     while (true) {
-      build_segment<GQA, P>(p, sh, hi, ow, tid, one_pass);
+      build_segment<GQA, KB, P, DRAFT>(p, sh, hi, ow, tid, one_pass);
       const int nseg = sh.nseg;
       if (warp == 0)
-        for (int t = 0; t < min(kStages, nseg); ++t) issue_item<GQA, KB, P>(p, sh, smem, x + t, t, policy, lane);
+        for (int t = 0; t < min(kStages, nseg); ++t) issue_item<GQA, KB, P, DRAFT>(p, sh, smem, x + t, t, policy, lane);
       int stg = x % kStages;
       uint32_t par = uint32_t(x / kStages) & 1u;
       for (int t = 0; t < nseg; ++t) {
@@ -1256,7 +1339,9 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
             const int pw = (32 * warp) / P, grp = ((32 * warp) % P) / 32;
             if (pw < n) page_group<T, GQA, KB, P>(sb + pw * R::record, grp, lq, qs, st, lane, p.err);
           } else if (int(d.w >> 16) % 4 == warp) {
-            residual_piece<T, GQA>(sb, sb + kPieceTokens * kResRowBytes, n, qs, st, lane, p.c_log2, p.err, p.sel != nullptr);
+            residual_piece<T, GQA, DRAFT>(sb, sb + kPieceTokens * kResRowBytes, n, qs, st, lane, p.c_log2, p.err,
+                                          DRAFT || p.sel != nullptr, sh.mk[DRAFT ? stg : 0], DRAFT ? sh.first[stg] : 0,
+                                          p.gqa_log2);
           }
         }
         // release the stage; the last warp to release it refills it with item xi + kStages
@@ -1266,7 +1351,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
         prev = __shfl_sync(kFull, prev, 0);
         if (prev == 3) {
           if (lane == 0) sh.rel[stg] = 0;
-          if (t + kStages < nseg) issue_item<GQA, KB, P>(p, sh, smem, xi + kStages, t + kStages, policy, lane);
+          if (t + kStages < nseg) issue_item<GQA, KB, P, DRAFT>(p, sh, smem, xi + kStages, t + kStages, policy, lane);
         }
         if (++stg == kStages) {
           stg = 0;
@@ -1303,7 +1388,8 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
           const int u = d.b * p.Hkv + d.h;
           const int i0 = int(d.io & 0xffffu), i1 = int(d.io >> 16);
           const bool sole = i0 == i1;
-          float* outu = p.out + (size_t(d.b) * p.Hq + size_t(d.h) * GQA) * kHeadDim;
+          float* outu = out_base<GQA, DRAFT>(p, d.b, d.h);
+          const int rows = out_rows<GQA, DRAFT>(p, d.b);
           float* part_me = p.part + (size_t(owner) + u) * GQA * kPartStride;
           for (int e = tid; e < GQA * kHeadDim; e += kDecodeThreads) {
             const int h = e >> 7, ch = e & 127;
@@ -1320,7 +1406,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
               }
             }
             if (sole) {
-              outu[e] = Ls > 0.0f ? O / Ls : 0.0f;
+              if (!DRAFT || h < rows) outu[out_row<DRAFT>(p, h) + ch] = Ls > 0.0f ? O / Ls : 0.0f;
             } else {
               float* pp = part_me + h * kPartStride;
               pp[ch] = O;
@@ -1342,7 +1428,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
                 sh.tail_io = d.io;
               }
             } else if (warp == 3) {
-              merge_partials<GQA>(p, u, i0, i1, outu, lane);
+              merge_partials<GQA, DRAFT>(p, u, i0, i1, outu, lane);
             }
           }
         }
@@ -1357,8 +1443,8 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
   if (sh.tail_u >= 0) {
     const int u = sh.tail_u, b = u / p.Hkv, h = u - b * p.Hkv;
     const uint32_t io = sh.tail_io;
-    merge_partials_cta<GQA>(p, &sh.arrived, u, int(io & 0xffffu), int(io >> 16),
-                            p.out + (size_t(b) * p.Hq + size_t(h) * GQA) * kHeadDim, warp, lane);
+    merge_partials_cta<GQA, DRAFT>(p, &sh.arrived, u, int(io & 0xffffu), int(io >> 16), out_base<GQA, DRAFT>(p, b, h),
+                                   warp, lane);
   }
 
   // ---------------------------------------------------------------- 3. leave
@@ -1375,10 +1461,10 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
 
 // ---------------------------------------------------------------- per-instantiation host side
 
-template <typename T, int GQA, int KB, int P>
+template <typename T, int GQA, int KB, int P, bool DRAFT>
 cudaError_t prepare_decode() {
   static int seen[64];
-  return ensure_dynamic_smem(decode_kernel<T, GQA, KB, P>, int(Smem<GQA, P, KB>::bytes), seen);
+  return ensure_dynamic_smem(decode_kernel<T, GQA, KB, P, DRAFT>, int(Smem<GQA, P, KB>::bytes), seen);
 }
 
 // Calls f.template operator()<KB, P>() for one (kb, P).
@@ -1407,23 +1493,23 @@ struct DecodeOcc {
   int* n;
   template <int KB, int P>
   cudaError_t operator()() {
-    cudaError_t e = prepare_decode<T, GQA, KB, P>();
+    cudaError_t e = prepare_decode<T, GQA, KB, P, false>();
     if (e != cudaSuccess) return e;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, decode_kernel<T, GQA, KB, P>, kDecodeThreads,
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, decode_kernel<T, GQA, KB, P, false>, kDecodeThreads,
                                                          Smem<GQA, P, KB>::bytes);
   }
 };
 
-template <typename T, int GQA>
+template <typename T, int GQA, bool DRAFT>
 struct DecodeRun {
   const DecodeParams& p;
   cudaStream_t stream;
   template <int KB, int P>
   cudaError_t operator()() {
     if (p.L.record != Rec<P, KB>::record || p.L.payload != Rec<P, KB>::payload) return cudaErrorInvalidValue;
-    cudaError_t e = prepare_decode<T, GQA, KB, P>();
+    cudaError_t e = prepare_decode<T, GQA, KB, P, DRAFT>();
     if (e != cudaSuccess) return e;
-    return launch_pdl(decode_kernel<T, GQA, KB, P>, dim3(p.n_ctas), dim3(kDecodeThreads), Smem<GQA, P, KB>::bytes,
+    return launch_pdl(decode_kernel<T, GQA, KB, P, DRAFT>, dim3(p.n_ctas), dim3(kDecodeThreads), Smem<GQA, P, KB>::bytes,
                       stream, p);
   }
 };
@@ -1434,7 +1520,12 @@ struct DecodeRun {
     return dispatch_kb_p(kb, P, DecodeOcc<T, GQA>{n});                                          \
   }                                                                                             \
   cudaError_t decode_launch_##NAME(const DecodeParams& p, cudaStream_t stream) {               \
-    return dispatch_kb_p(p.KB, p.P, DecodeRun<T, GQA>{p, stream});                              \
+    return dispatch_kb_p(p.KB, p.P, DecodeRun<T, GQA, false>{p, stream});                       \
+  }
+// ... and one the launch for drafted tokens.
+#define KVQ_DRAFT_INSTANCE(NAME, T, GQA)                                                        \
+  cudaError_t draft_launch_##NAME(const DecodeParams& p, cudaStream_t stream) {                 \
+    return dispatch_kb_p(p.KB, p.P, DecodeRun<T, GQA, true>{p, stream});                        \
   }
 
 }  // namespace kvq

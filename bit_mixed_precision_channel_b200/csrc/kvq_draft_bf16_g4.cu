@@ -1,0 +1,6 @@
+// Decode-attention kernels with drafted tokens for bf16 caches, 4 rows (drafted token, query head) per kv head.
+#include "kvq_decode_impl.cuh"
+
+namespace kvq {
+KVQ_DRAFT_INSTANCE(bf16_g4, __nv_bfloat16, 4)
+}  // namespace kvq

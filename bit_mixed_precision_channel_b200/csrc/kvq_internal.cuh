@@ -351,6 +351,13 @@ struct DecodeParams {
   const int32_t* sel;
   const int32_t* table_len;
   int table_pages;
+  // drafted tokens (few rows of tree attention): [batch][T][Hkv][128], one mask word a token;
+  // q and out are [batch][T][Hq][128], and a unit's heads are (token, query head), token first
+  const uint16_t* k_draft;
+  const uint16_t* v_draft;
+  const uint32_t* mask;
+  const int32_t* draft_len;
+  int T, gqa_log2;
 };
 
 // Choice of pages by the largest logits their key ranges allow.
@@ -405,6 +412,7 @@ cudaError_t launch_tree(const TreeParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_flush_commit(int32_t* res_len, const int32_t* new_page, int32_t* page_table, int max_pages,
                                 int32_t* num_pages, long long pool_pages, int batch, int P, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams& p, int gqa, int dtype, cudaStream_t stream);
+cudaError_t launch_draft(const DecodeParams& p, int rows, int dtype, cudaStream_t stream);
 cudaError_t launch_prefill(const void* q, const void* k, const void* v, int L, int Hq, int Hkv, float sm_scale,
                            int dtype, float* out, float* lse, float* score, cudaStream_t stream);
 cudaError_t launch_retain(const float* score, int L, int Hkv, int n_heavy, int n_recent, int32_t* keep,

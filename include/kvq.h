@@ -430,9 +430,12 @@ KVQ_API kvq_status kvq_decode_attention_sparse(const kvq_config* cfg, const void
 /* Most drafted tokens of a sequence. */
 #define KVQ_MAX_DRAFT 128
 
-/* Scratch bytes of kvq_tree_attention on the current device, 0 for arguments it rejects.
- * The contents need no preparation and carry nothing from call to call; calls that may
- * overlap on the GPU need a workspace each. */
+/* Scratch bytes of kvq_tree_attention on the current device, 0 for arguments it rejects.  Its
+ * first 64 KiB hold arrival counters, which must be zero before the first call (clear the
+ * workspace once after allocating it, and after a call that raised KVQ_DEV_ERR_TIMEOUT);
+ * every call leaves them zero.  The rest carries nothing from call to call, so calls of
+ * different shapes may take turns in one workspace of the largest size; calls that may
+ * overlap on the GPU need one each. */
 KVQ_API size_t kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n_draft);
 
 /* Attention of a tree of drafted tokens over the cache: for every sequence b, drafted token

@@ -30,7 +30,8 @@ def make(cfg, pages, window, T, drafts, seed, sees=None, chain=False, **more):
     dt = cfg.dtype
     c.t = dict(q=to_dev(c.q, dt), k_draft=to_dev(c.k, dt), v_draft=to_dev(c.v, dt),
                mask=torch.from_numpy(pack_mask(c.sees)).cuda(), draft_len=c.ints(drafts))
-    c.ws = torch.full((kb.tree_workspace_bytes(cfg, B, T),), 0xff, dtype=torch.uint8, device="cuda")
+    c.ws = torch.zeros(kb.tree_workspace_bytes(cfg, B, T), dtype=torch.uint8, device="cuda")
+    c.ws[65536:] = 0xff  # behind the counters nothing has to be prepared
     c.out = torch.full((B, T, cfg.num_q_heads, D), 7.5, device="cuda")
     return c
 
@@ -44,6 +45,7 @@ def call(c, **over):
 
 
 def check(c, out=None, rows=None, sm_scale=None):
+    assert not c.ws[:65536].any(), "counters left behind"
     out = (c.out if out is None else out).cpu().numpy()
     cfg = c.cfg
     more = {} if sm_scale is None else dict(sm_scale=sm_scale)
@@ -75,6 +77,14 @@ def check(c, out=None, rows=None, sm_scale=None):
     (kb.BF16, 1, 1, 32, 0, 40, [1, 4], [0, 9], [40, 39]),
     (kb.BF16, 1, 2, 128, 128, 5, [3], [16], [5]),
     (kb.F16, 1, 8, 64, 16, 20, [0], [0], [20]),              # nothing but the drafted tokens
+    # at most 8 rows of a kv head
+    (kb.F16, 2, 4, 128, 32, 2, [9, 0, 40], [127, 128, 3], [2, 1, 2]),
+    (kb.BF16, 2, 2, 64, 64, 4, [7, 1, 0], [64, 15, 0], [4, 3, 0]),
+    (kb.F16, 1, 1, 32, 0, 8, [50, 2, 0], [31, 8, 0], [8, 5, 7]),
+    (kb.BF16, 2, 8, 128, 16, 1, [33, 1, 0], [126, 0, 1], [1, 1, 0]),
+    (kb.BF16, 1, 1, 32, 128, 3, [12], [32], [3]),
+    (kb.F16, 3, 2, 64, 32, 3, [5, 6], [61, 62], [3, 2]),
+    (kb.F16, 1, 1, 128, 32, 9, [3], [40], [9]),              # one row more
 ])
 def test_matches_64_bits(dtype, H, gqa, P, k, T, pages, window, drafts):
     cfg = kb.Config(num_q_heads=gqa * H, num_kv_heads=H, page_tokens=P, num_boost=k, dtype=dtype)
@@ -106,10 +116,11 @@ def test_many_sequences():
     check(c)
 
 
-def test_rows_whose_mask_leaves_nothing():
+@pytest.mark.parametrize("gqa", [1, 4])
+def test_rows_whose_mask_leaves_nothing(gqa):
     """Without a cache, a token whose mask is empty has nothing to attend to: zero.  With one, it
     attends to the cache alone.  Bits at or behind draft_len name no token."""
-    cfg = kb.Config(num_q_heads=4, num_kv_heads=1, page_tokens=32, num_boost=16)
+    cfg = kb.Config(num_q_heads=gqa, num_kv_heads=1, page_tokens=32, num_boost=16)
     sees = np.zeros((2, 8, 8), bool)
     sees[:, 2, 1] = sees[:, 4, 4] = True
     sees[:, 5, 7] = True  # behind draft_len
@@ -122,8 +133,9 @@ def test_rows_whose_mask_leaves_nothing():
 
 
 @pytest.mark.parametrize("dtype", [kb.F16, kb.BF16])
-def test_a_token_no_row_sees_may_hold_anything(dtype):
-    cfg = kb.Config(num_q_heads=4, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=dtype)
+@pytest.mark.parametrize("gqa", [1, 4])
+def test_a_token_no_row_sees_may_hold_anything(dtype, gqa):
+    cfg = kb.Config(num_q_heads=gqa, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=dtype)
     sees = np.tril(np.ones((1, 6, 6), bool))
     sees[:, :, 3] = False
     c = make(cfg, [2], [4], 6, [6], seed=2, sees=sees)
@@ -137,9 +149,10 @@ def test_a_token_no_row_sees_may_hold_anything(dtype):
     check(c)
 
 
-def test_large_values_and_queries():
+@pytest.mark.parametrize("gqa", [1, 4])
+def test_large_values_and_queries(gqa):
     """Values of magnitude 3e3 and queries of 200: the softmax turns into the largest logit's value."""
-    cfg = kb.Config(num_q_heads=4, num_kv_heads=1, page_tokens=32, num_boost=16)
+    cfg = kb.Config(num_q_heads=gqa, num_kv_heads=1, page_tokens=32, num_boost=16)
     c = make(cfg, [4], [9], 4, [4], seed=4)
     c.q = c.queries(1, 4, scale=200.0)
     c.v = syn.to_bits(3e3 * c.rng.standard_normal((1, 4, 1, D)).astype(np.float32), cfg.dtype)
@@ -170,10 +183,11 @@ def test_pages_of_wide_value_ranges(dtype):
     check(c)
 
 
-def test_negative_and_zero_scale():
-    cfg = kb.Config(num_q_heads=4, num_kv_heads=2, page_tokens=32, num_boost=16)
+@pytest.mark.parametrize("T", [2, 5])
+def test_negative_and_zero_scale(T):
+    cfg = kb.Config(num_q_heads=8, num_kv_heads=2, page_tokens=32, num_boost=16)
     for sm in (-0.05, 0.0, 1.0):
-        c = make(cfg, [3], [7], 5, [5], seed=9)
+        c = make(cfg, [3], [7], T, [T], seed=9)
         call(c, sm_scale=sm)
         torch.cuda.synchronize()
         assert c.err.item() == 0
@@ -198,8 +212,9 @@ def test_one_token_equals_the_step_after_its_append():
     assert (out - c.out[:, 0]).abs().max() <= 4e-3
 
 
-def test_device_errors_are_flagged_and_leave_other_sequences_right():
-    cfg = kb.Config(num_q_heads=4, num_kv_heads=1, page_tokens=32, num_boost=16)
+@pytest.mark.parametrize("gqa", [1, 4])
+def test_device_errors_are_flagged_and_leave_other_sequences_right(gqa):
+    cfg = kb.Config(num_q_heads=gqa, num_kv_heads=1, page_tokens=32, num_boost=16)
     for name, value, flag in (("num_pages", 99, kb.DEV_ERR_LENGTH), ("num_pages", -1, kb.DEV_ERR_LENGTH),
                               ("res_len", 33, kb.DEV_ERR_LENGTH), ("res_len", -2, kb.DEV_ERR_LENGTH),
                               ("draft_len", 6, kb.DEV_ERR_LENGTH), ("draft_len", -1, kb.DEV_ERR_LENGTH),
@@ -222,15 +237,16 @@ def test_device_errors_are_flagged_and_leave_other_sequences_right():
             K = np.concatenate([K, syn.from_bits(c.k[b, :n, 0], cfg.dtype).astype(np.float64)])
             V = np.concatenate([V, syn.from_bits(c.v[b, :n, 0], cfg.dtype).astype(np.float64)])
             sees = np.concatenate([np.ones(len(K) - n, bool), c.sees[b, n - 1, :n]])
-            want, tol = attend(syn.from_bits(c.q[b, n - 1, 2], cfg.dtype).astype(np.float64), K, V, sees)
-            assert_row(got[i, n - 1, 2].cpu().numpy(), want, tol, f"{name}: sequence {b}")
+            want, tol = attend(syn.from_bits(c.q[b, n - 1, gqa - 1], cfg.dtype).astype(np.float64), K, V, sees)
+            assert_row(got[i, n - 1, gqa - 1].cpu().numpy(), want, tol, f"{name}: sequence {b}")
         assert keep == (c.B, c.drafts)
 
 
-def test_same_bits_again_on_another_stream_and_replayed():
+@pytest.mark.parametrize("T,drafts", [(12, [12, 7]), (2, [2, 1])])
+def test_same_bits_again_on_another_stream_and_replayed(T, drafts):
     """Nothing depends on the order of atomics, on the stream, or on what the workspace held."""
     cfg = kb.Config(num_q_heads=8, num_kv_heads=2, page_tokens=128, num_boost=32)
-    c = make(cfg, [40, 3], [17, 90], 12, [12, 7], seed=14, distinct=9)
+    c = make(cfg, [40, 3], [17, 90], T, drafts, seed=14, distinct=9)
     call(c)
     torch.cuda.synchronize()
     first = c.out.clone()
@@ -238,7 +254,7 @@ def test_same_bits_again_on_another_stream_and_replayed():
     s.wait_stream(torch.cuda.current_stream())
     other = torch.full_like(c.out, 7.5)
     with torch.cuda.stream(s):
-        c.ws.fill_(0x5a)
+        c.ws[65536:] = 0x5a
         call(c, out=other)
     s.synchronize()
     assert torch.equal(first, other)
@@ -270,10 +286,47 @@ def test_two_calls_at_once_with_a_workspace_each():
     for s in streams:
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
-            ws = torch.empty_like(c.ws)
+            ws = torch.zeros_like(c.ws)
             for _ in range(4):
                 out = torch.full_like(c.out, 7.5)
                 call(c, out=out, workspace=ws)
                 outs.append((out, ws))
     torch.cuda.synchronize()
     assert all(torch.equal(o, c.out) for o, _ in outs)
+
+
+def test_shapes_take_turns_in_one_workspace():
+    """Few rows (counters) and many (cut units), small and large batches, on the same scratch."""
+    cs = []
+    for B, gqa, T in ((2, 4, 2), (2, 4, 20), (40, 1, 3), (1, 8, 1), (3, 8, 60)):
+        cfg = kb.Config(num_q_heads=2 * gqa, num_kv_heads=2, page_tokens=64, num_boost=16)
+        cs.append(make(cfg, [(7 * b) % 30 for b in range(B)], [(5 * b) % 64 for b in range(B)], T, [T] * B, seed=B + T, distinct=12))
+    ws = torch.zeros(max(c.ws.numel() for c in cs), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for c in cs:
+            c.ws = ws
+            c.out.fill_(7.5)
+            call(c)
+    torch.cuda.synchronize()
+    for c in cs:
+        assert c.err.item() == 0
+        check(c, rows=[0])
+
+
+def test_more_units_than_counters():
+    """A batch whose arrival counters do not fit their place at the workspace's start."""
+    cfg = kb.Config(num_q_heads=8, num_kv_heads=8, page_tokens=32, num_boost=0)
+    B = 2100
+    c = make(cfg, [2 if b % 700 == 0 else 0 for b in range(B)], [b % 3 for b in range(B)], 1, [1] * B, seed=3, distinct=4)
+    call(c)
+    call(c)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    keep = [0, 1, 2, 700, 1400, 2099]
+    got = c.out
+    for b in keep:
+        K, V = c.rows(b, 3)
+        K = np.concatenate([K, syn.from_bits(c.k[b, :1, 3], cfg.dtype).astype(np.float64)])
+        V = np.concatenate([V, syn.from_bits(c.v[b, :1, 3], cfg.dtype).astype(np.float64)])
+        want, tol = attend(syn.from_bits(c.q[b, 0, 3], cfg.dtype).astype(np.float64), K, V)
+        assert_row(got[b, 0, 3].cpu().numpy(), want, tol, f"sequence {b}")
