@@ -57,7 +57,8 @@ constexpr int kThreads = 896;  // 7 warpgroups: two of softmax, four of dequant,
 // next to no L1, so a register spilled in a role's loop costs an L2 access.
 constexpr int kRegsLaunch = 72, kRegsSoft = 112, kRegsDeq = 56, kRegsRest = 56;
 static_assert(2 * kRegsSoft + 4 * kRegsDeq + kRegsRest <= 7 * kRegsLaunch, "register split");
-constexpr int kRecStages = 3;
+// (two where every channel may be boosted: the moves take the third's place)
+constexpr int rec_stages(int KB) { return KB == 8 ? 2 : 3; }
 // The tensor cores round their fp32 accumulator toward zero: 16 products a tile shrink a long
 // sum by about 2^-24 each.  O is therefore moved every kFlush tiles into fp32 sums in shared
 // memory, which round to nearest.  (Left in tensor memory over 28 tiles of a 4096-token
@@ -332,14 +333,15 @@ __device__ __forceinline__ void line_find(const TreeParams& p, Line& ln, int cta
 
 // Moves of one page's boosted codes, by the words that receive them (8 lists, see
 // list_moves): {rotation | source word << 8, mask}, padded to an even length.
+// n[0] = -1: every channel boosted, row j of plane B being channel j.
 struct Moves {
   uint2 m[8][18];
   int n[8];
 };
 
-// MOVES: whether the kernel lists moves (some but not all channels boosted).
-template <bool MOVES>
+template <int KB>
 struct Shared {
+  static constexpr int kRecStages = rec_stages(KB);
   uint64_t rec_full[kRecStages], rec_empty[kRecStages], mv_full[kRecStages], k_full, k_empty, v_full, v_empty, s_full[2],
       p_full[2], pv_done[2], q_full;
   uint32_t tmem;
@@ -349,7 +351,7 @@ struct Shared {
   float smax[3][4];                     // largest value scale of a page tile's groups
   float xs[3][kDeqWarps];               // the same of a raw tile, by the warp that wrote it
   Line line;
-  __align__(16) Moves moves[MOVES ? kRecStages : 1][MOVES ? 4 : 1];  // [stage][page of the tile]
+  __align__(16) Moves moves[KB > 0 ? kRecStages : 1][KB > 0 ? 4 : 1];  // [stage][page of the tile]
 };
 
 // Waits for a phase (about a second at most); false once any wait of the CTA has given up,
@@ -386,6 +388,14 @@ constexpr int kPart = 132;  // floats of a partial row: unnormalised output, ref
 // code to that bit.  One warp lists a page's moves; the indices are those of the record.
 template <int KB>
 __device__ __forceinline__ void list_moves(const uint8_t* idx, Moves& mv, int lane) {
+  if constexpr (KB == 8) {
+    // (not so with fewer boosted channels of a head than the record has rows)
+    if (__all_sync(kFull, lds32(idx + 4 * lane) == 0x03020100u + 0x04040404u * uint32_t(lane))) {
+      if (lane == 0) mv.n[0] = -1;
+      __syncwarp();
+      return;
+    }
+  }
   int count = 0;  // of list `lane`
 #pragma unroll 1
   for (int j0 = 0; j0 < 16 * KB; j0 += 32) {
@@ -426,13 +436,13 @@ __device__ __forceinline__ void key_row(const TreeParams& p, const uint8_t* rec,
   const uint4 w0 = lds128(rec + p.L.k_codes + tp * 32), w1 = lds128(rec + p.L.k_codes + tp * 32 + 16);
   const uint32_t w[4] = {half ? w0.y : w0.x, half ? w0.w : w0.z, half ? w1.y : w1.x, half ? w1.w : w1.z};
   uint32_t wb[4];
-  if constexpr (KB == 8) {  // every channel boosted: plane B has the layout of plane A
+  if (KB == 8 && mv.n[0] < 0) {  // plane B has the layout of plane A
     const uint4 b0 = lds128(rec + p.L.kb_codes + tp * 32), b1 = lds128(rec + p.L.kb_codes + tp * 32 + 16);
     wb[0] = (half ? b0.y : b0.x) >> (2 * a);
     wb[1] = (half ? b0.w : b0.z) >> (2 * a);
     wb[2] = (half ? b1.y : b1.x) >> (2 * a);
     wb[3] = (half ? b1.w : b1.z) >> (2 * a);
-  } else if constexpr (KB > 0) {
+  } else if (KB > 0) {
     const uint8_t* brow = rec + p.L.kb_codes + tp * (4 * KB);
     uint32_t src0 = 0u, src1 = 0u;
     if constexpr (KB == 1) src0 = lds32(brow);
@@ -571,8 +581,9 @@ template <typename T, int KB>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr bool kMoves = KB > 0 && KB < 8;
-  __shared__ Shared<kMoves> sh;
+  constexpr bool kMoves = KB > 0;
+  constexpr int kRecStages = rec_stages(KB);
+  __shared__ Shared<KB> sh;
   // (taken from lane 0, so that the compiler knows the roles' branches to be uniform)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
 
@@ -1247,7 +1258,7 @@ static __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant
 template <typename T, int KB>
 cudaError_t launch_t(const TreeParams& p, cudaStream_t stream) {
   static int seen[64];
-  const int bytes = int(kRec + kRecStages * uint32_t(128 / p.P) * p.L.record);
+  const int bytes = int(kRec + rec_stages(KB) * uint32_t(128 / p.P) * p.L.record);
   cudaError_t e = ensure_dynamic_smem(tree_kernel<T, KB>, bytes, seen);
   if (e != cudaSuccess) return e;
   // the register split waits for good on a build that launches with fewer registers

@@ -29,7 +29,8 @@ class Cache:
     """Pages of random keys and values quantized by the oracle, with a window, on the device."""
 
     def __init__(self, cfg: kb.Config, pages, window, seed: int, distinct: int | None = None, garbage: bool = True,
-                 device="cuda"):
+                 device="cuda", boosts=None):
+        """boosts: boosted channels of each head (num_boost of all)."""
         self.cfg, self.rng = cfg, np.random.default_rng(seed)
         rng, H, P, dt = self.rng, cfg.num_kv_heads, cfg.page_tokens, cfg.dtype
         self.B, self.pages, self.window = len(pages), list(pages), list(window)
@@ -41,7 +42,7 @@ class Cache:
         for i in range(pool_pages):
             K, V = self.tokens(P), syn.to_bits(rng.standard_normal((P, H, D)).astype(np.float32), dt)
             for h in range(H):
-                self.pool[i, h] = oracle.quantize_page(K[:, h], V[:, h], self.oc)
+                self.pool[i, h] = oracle.quantize_page_ex(K[:, h], V[:, h], self.oc, boosts and boosts[h])
         if distinct is None:
             order = rng.permutation(pool_pages)
         else:

@@ -88,6 +88,19 @@ def test_choice_equals_the_64_bit_ranking(dtype, H, gqa, P, k, pages, select, fi
     np.testing.assert_array_equal(sel.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("k,boosts", [(128, [0, 100]), (16, [3, 16])])
+def test_choice_among_heads_with_fewer_boosted_channels(k, boosts):
+    cfg = kb.Config(num_q_heads=4, num_kv_heads=2, page_tokens=64, num_boost=k)
+    c = Cache(cfg, [50, 7], [0, 0], seed=k, boosts=boosts)
+    q = c.queries(2)
+    sel, n_sel = run_select(c, q, 9, 0, 1)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    want, counts = choose(c, q, 9, 0, 1)
+    np.testing.assert_array_equal(n_sel.cpu().numpy(), counts)
+    np.testing.assert_array_equal(sel.cpu().numpy(), want)
+
+
 def test_zero_query_ties_everywhere():
     """Every score is zero, of either sign: the lowest slots are chosen."""
     cfg = kb.Config(num_q_heads=2, num_kv_heads=1, page_tokens=32, num_boost=16)

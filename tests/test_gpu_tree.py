@@ -95,6 +95,23 @@ def test_matches_64_bits(dtype, H, gqa, P, k, T, pages, window, drafts):
     check(c)
 
 
+@pytest.mark.parametrize("T,gqa", [(9, 4), (2, 4)])
+@pytest.mark.parametrize("dtype,P,k,boosts", [
+    (kb.F16, 32, 128, [0, 5, 100, 128]),
+    (kb.BF16, 128, 128, [127, 1, 64, 0]),
+    (kb.F16, 64, 64, [63, 0, 64, 17]),
+    (kb.BF16, 32, 16, [0, 1, 15, 16]),
+])
+def test_heads_with_fewer_boosted_channels(dtype, P, k, boosts, T, gqa):
+    """Records with rows for more boosted channels than the head has: the rows in use name any channel."""
+    cfg = kb.Config(num_q_heads=4 * gqa, num_kv_heads=4, page_tokens=P, num_boost=k, dtype=dtype)
+    c = make(cfg, [11, 2], [9, 0], T, [T, T], seed=k + P, boosts=boosts)
+    call(c)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    check(c)
+
+
 def test_long_sequences_beside_short_ones_are_split():
     cfg = kb.Config(num_q_heads=4, num_kv_heads=1, page_tokens=128, num_boost=32)
     c = make(cfg, [120, 0, 1, 64], [1, 3, 0, 127], 24, [24, 24, 5, 1], seed=3, distinct=12)
