@@ -101,9 +101,15 @@ class Config:
         a serving step makes the same call for every layer."""
         m = self.__dict__.get("_m")
         if m is None:
-            m = (ctypes.byref(self.c()), torch_dtype(self.dtype), self.num_kv_heads * page_bytes(self))
+            c = ctypes.byref(self.c())
+            _check("kvq_check_config", load().kvq_check_config(c))
+            m = (c, torch_dtype(self.dtype), self.num_kv_heads * page_bytes(self))
             object.__setattr__(self, "_m", m)
         return m
+
+    def __getstate__(self):
+        """For copies and pickles: without _marshalled's pointer."""
+        return {k: v for k, v in self.__dict__.items() if k != "_m"}
 
 
 def torch_dtype(dtype: int) -> torch.dtype:

@@ -176,3 +176,21 @@ def test_binding_refuses(fn, make, over, msg):
 def test_well_formed_tensors_fail_only_on_the_device_check(fn, make):
     with pytest.raises(ValueError, match="CUDA tensors"):
         fn(CFG, **make())
+
+
+def test_a_config_that_was_used_can_be_copied_and_pickled(lib):
+    import copy
+    import pickle
+    cfg = kb.Config(num_q_heads=8, num_kv_heads=2, page_tokens=32, num_boost=16)
+    cfg._marshalled()
+    for other in (copy.copy(cfg), copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg))):
+        assert other == cfg and hash(other) == hash(cfg)
+        assert other._marshalled()[1:] == cfg._marshalled()[1:]
+
+
+def test_a_config_the_library_does_not_take_is_named(lib):
+    for cfg in (kb.Config(head_dim=64), kb.Config(num_boost=7), kb.Config(num_q_heads=7, num_kv_heads=2)):
+        z = torch.zeros(1)
+        for call in (lambda: kb.select_pages(cfg, z, z, z, z, z, z), lambda: kb.append_path(cfg, z, z, z, z, z, z, z, z)):
+            with pytest.raises(kb.KVQError, match="kvq_check_config"):
+                call()
