@@ -101,6 +101,38 @@ def test_choice_among_heads_with_fewer_boosted_channels(k, boosts):
     np.testing.assert_array_equal(sel.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("B", [160, 330, 650])
+def test_choice_with_more_sequences_than_clusters_of_eight(B):
+    """Many sequences: fewer blocks share a sequence's pages, down to one; both ways to select."""
+    cfg = kb.Config(num_q_heads=2, num_kv_heads=1, page_tokens=32, num_boost=16)
+    rng = np.random.default_rng(B)
+    c = Cache(cfg, rng.choice([0, 3, 7, 40, 255, 256, 257, 300], B).tolist(), [0] * B, seed=B, distinct=25)
+    q = c.queries(B)
+    sel, n_sel = run_select(c, q, 6, 1, 1)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    want, counts = choose(c, q, 6, 1, 1)
+    np.testing.assert_array_equal(n_sel.cpu().numpy(), counts)
+    np.testing.assert_array_equal(sel.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("n", [200, 5000, 204800])
+def test_the_largest_page_table(n):
+    """A table as long as the call allows, with few pages in it and with all."""
+    cfg = kb.Config(num_q_heads=1, num_kv_heads=1, page_tokens=32, num_boost=0)
+    c = Cache(cfg, [n, 12], [0, 0], seed=n, distinct=30)
+    table = np.full((2, 204800), -1, np.int32)
+    table[:, :min(c.max_pages, 204800)] = c.table[:, :204800]
+    c.d["page_table"] = c.ints(table)
+    q = c.queries(2)
+    sel, n_sel = run_select(c, q, 50, 2, 3)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    want, counts = choose(c, q, 50, 2, 3)
+    np.testing.assert_array_equal(n_sel.cpu().numpy(), counts)
+    np.testing.assert_array_equal(sel.cpu().numpy(), want)
+
+
 def test_zero_query_ties_everywhere():
     """Every score is zero, of either sign: the lowest slots are chosen."""
     cfg = kb.Config(num_q_heads=2, num_kv_heads=1, page_tokens=32, num_boost=16)

@@ -133,6 +133,19 @@ def test_many_sequences():
     check(c)
 
 
+def test_more_sequences_than_threads():
+    cfg = kb.Config(num_q_heads=1, num_kv_heads=1, page_tokens=32, num_boost=16)
+    B = 2000
+    rng = np.random.default_rng(9)
+    pages, window, drafts = rng.integers(0, 4, B), rng.integers(0, 33, B), rng.integers(0, 10, B)
+    pages[1100:1900] = window[1100:1900] = drafts[1100:1900] = 0
+    c = make(cfg, pages.tolist(), window.tolist(), 9, drafts.tolist(), seed=5, distinct=20, chain=True)
+    call(c)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    check(c, rows=[0, 8])
+
+
 @pytest.mark.parametrize("gqa", [1, 4])
 def test_rows_whose_mask_leaves_nothing(gqa):
     """Without a cache, a token whose mask is empty has nothing to attend to: zero.  With one, it
