@@ -194,6 +194,11 @@ __device__ __forceinline__ uint32_t half_of(uint32_t x) {  // x / 2 of an fp16 p
   return h2_as_u32(__hmul2(u32_as_h2(x), __float2half2_rn(0.5f)));
 }
 
+// Whether an element of the fp16 pair is no finite number.
+__device__ __forceinline__ bool not_finite2(uint32_t x) {
+  return (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u;
+}
+
 // Tiles of one unit of sequence b; 0 units for invalid lengths or no drafted token.
 struct Seq {
   int np, rl, dl;
@@ -814,9 +819,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (half == 0 && a == 0) {
           if (have && lane < 16) {  // zero points: row 128 + g of the key operand
             const uint4 z = lds128(rec + p.L.k_zero + gp * 256 + 16 * lane);
-            *reinterpret_cast<uint4*>(smem + kKhi + tco(128 + g, lane)) =
-                make_uint4(half_of(meta_h2(z.x, T())), half_of(meta_h2(z.y, T())), half_of(meta_h2(z.z, T())),
-                           half_of(meta_h2(z.w, T())));
+            const uint4 o = make_uint4(half_of(meta_h2(z.x, T())), half_of(meta_h2(z.y, T())),
+                                       half_of(meta_h2(z.z, T())), half_of(meta_h2(z.w, T())));
+            // (a scale beyond fp16 makes the sums no number; a zero point could leave a weight of zero)
+            if (not_finite2(o.x) || not_finite2(o.y) || not_finite2(o.z) || not_finite2(o.w))
+              flag_error(p.err, KVQ_DEV_ERR_RANGE);
+            *reinterpret_cast<uint4*>(smem + kKhi + tco(128 + g, lane)) = o;
           }
         } else if (half == 1 && a == 0) {
           float s = 0.0f, z = 0.0f;
@@ -860,11 +868,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (it > 0 && !wait_warp(sh, &sh.k_empty, uint32_t(it - 1) & 1u)) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t k[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t k[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
           uint8_t* dst = smem + kKhi + tco(t0 + 2 * i, c & ~3) + 4 * (c & 3);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)  // pair e of 8 channels c: the operand's order
-            *reinterpret_cast<uint32_t*>(dst + 128 * e) = scaled_h2(k[e], 0.5f, T());
+          for (int e = 0; e < 4; ++e) {  // pair e of 8 channels c: the operand's order
+            k[e] = scaled_h2(k[e], 0.5f, T());
+            *reinterpret_cast<uint32_t*>(dst + 128 * e) = k[e];
+          }
+          const int xi = x0 + 2 * i;
+          if ((not_finite2(k[0]) || not_finite2(k[1]) || not_finite2(k[2]) || not_finite2(k[3])) &&
+              (xi < wk.s.rl || seen_by_any(p, wk.b, wk.s.dl, xi - wk.s.rl)))
+            flag_error(p.err, KVQ_DEV_ERR_RANGE);
         }
         // the values: what is no number is zero (a probability of zero has to stay zero), and
         // bf16 is brought below 2 by the token's power of two

@@ -131,7 +131,7 @@ typedef enum { KVQ_F16 = 0, KVQ_BF16 = 1 } kvq_dtype;
 #define KVQ_DEV_ERR_TABLE_FULL   4  /* flush with no free page-table slot or no destination page      */
 #define KVQ_DEV_ERR_TIMEOUT      8  /* a bounded wait for an asynchronous copy gave up                */
 #define KVQ_DEV_ERR_LENGTH      16  /* num_pages[b], res_len[b] or a per-head boost count out of range */
-#define KVQ_DEV_ERR_RANGE       32  /* decode: an operand outside the range the kernel carries (see
+#define KVQ_DEV_ERR_RANGE       32  /* an operand outside the range the kernel carries (see
                                        kvq_decode_attention, "Precision")                             */
 
 /* Shape and precision of one attention layer's KV cache.
@@ -452,7 +452,14 @@ KVQ_API size_t kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t batch, in
  * KVQ_MAX_DRAFT (KVQ_ERR_UNSUPPORTED above).  Rows i >= draft_len[b] of out are left as they
  * were, and nothing of the drafted tokens behind draft_len[b] or of window rows behind
  * res_len[b] takes part, whatever it holds.  A row that sees no token at all is zero.
- * Invalid lengths set KVQ_DEV_ERR_LENGTH, and the sequence's rows are left as they were. */
+ * Invalid lengths set KVQ_DEV_ERR_LENGTH, and the sequence's rows are left as they were.
+ * Precision and range: up to 8 rows of a KV head (n_draft * Hq / Hkv) as for
+ * kvq_decode_attention, on its kernel.  With more, half of a dequantized key (and q * 2^-e,
+ * e as there) enters as fp16, the codes times their scale as a high and a low part, the
+ * probabilities times their value scale as a high and a low part, sums and softmax
+ * statistics in fp32.  A group of keys that spans more than 130944, a key or zero point
+ * above 131008 in magnitude (bf16), and whatever a row sees that is not finite set
+ * KVQ_DEV_ERR_RANGE (the output is then undefined). */
 KVQ_API kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
                                       int32_t n_draft, int32_t batch, const int32_t* page_table,
                                       int32_t max_pages, const int32_t* num_pages, const void* res_k,

@@ -213,6 +213,38 @@ def test_pages_of_wide_value_ranges(dtype):
     check(c)
 
 
+@pytest.mark.parametrize("where", ["window", "drafted", "page", "nowhere"])
+@pytest.mark.parametrize("dtype", [kb.F16, kb.BF16])
+def test_keys_beyond_the_range_are_flagged_whatever_the_query(where, dtype):
+    """A key no operand holds meets a query so small that its logit is ordinary: never a quiet weight of zero."""
+    cfg = kb.Config(num_q_heads=8, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=dtype)
+    big = -2e5 if dtype == kb.BF16 else -6e4  # fp16: the largest keys are in range
+    c = make(cfg, [2], [4], 4, [4], seed=21)
+    import oracle
+    c.q[:] = 0
+    c.q[..., 7] = syn.to_bits(np.float32([1e-4]), dtype)[0]
+    c.t["q"] = to_dev(c.q, dtype)
+    one = syn.to_bits(np.float32([big]), dtype)[0]
+    if where == "window":
+        c.res_k[0, :, 2, 7] = one
+        c.d["res_k"] = to_dev(c.res_k, dtype)
+    elif where == "drafted":
+        c.k[0, 0, :, 7] = one
+        c.t["k_draft"] = to_dev(c.k, dtype)
+    elif where == "page":
+        K = c.tokens(32)[:, 0]
+        K[:, 7] = one
+        c.pool[c.table[0, 1], 0] = oracle.quantize_page(K, c.values(32)[:, 0], c.oc)
+        c.d["pool"] = torch.from_numpy(c.pool.reshape(-1)).cuda()
+    call(c)
+    torch.cuda.synchronize()
+    if dtype == kb.BF16 and where != "nowhere":
+        assert c.err.item() == kb.DEV_ERR_RANGE
+    else:
+        assert c.err.item() == 0
+        check(c)
+
+
 @pytest.mark.parametrize("T", [2, 5])
 def test_negative_and_zero_scale(T):
     cfg = kb.Config(num_q_heads=8, num_kv_heads=2, page_tokens=32, num_boost=16)
