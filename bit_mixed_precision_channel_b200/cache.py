@@ -41,8 +41,10 @@ class PagedKVCache:
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.new_page = torch.full((batch,), -1, dtype=torch.int32, device=self.device)
         self.counters = torch.zeros(batch, dtype=torch.int32, device=self.device)  # append_flush arrivals
-        # speculative decoding: the last choice of pages, the accepted lengths, the tree's scratch
+        # speculative decoding: the last choice of pages and the buffer of every size asked for, the
+        # accepted lengths, the tree's scratch.  Captured graphs may hold these buffers: none is replaced.
         self.sel = None
+        self.choices = {}
         self.n_sel = torch.zeros(batch, dtype=torch.int32, device=self.device)
         self.n_path = torch.zeros(batch, dtype=torch.int32, device=self.device)
         self.taken = torch.zeros(batch, dtype=torch.int32, device=self.device)
@@ -172,8 +174,13 @@ class PagedKVCache:
         allow q the largest logits (the first n_first and the last n_recent always): fills
         and returns self.sel [B][Hkv][n_select] and self.n_sel [B].  A choice stays valid
         while pages are only appended."""
-        if self.sel is None or self.sel.shape[2] != n_select:
-            self.sel = torch.empty(self.batch, self.cfg.num_kv_heads, n_select, dtype=torch.int32, device=self.device)
+        if n_select not in self.choices:
+            if n_select < 1:
+                raise ValueError(f"n_select is {n_select}: at least one page")
+            with self._on(stream):
+                self.choices[n_select] = torch.empty(self.batch, self.cfg.num_kv_heads, n_select, dtype=torch.int32,
+                                                     device=self.device)
+        self.sel = self.choices[n_select]
         kb.select_pages(self.cfg, self.pool, q, self.page_table, self.num_pages, self.sel, self.n_sel, n_first, n_recent,
                         self.err, stream)
         return self.sel, self.n_sel
@@ -187,10 +194,14 @@ class PagedKVCache:
 
     def verify(self, q, k_draft, v_draft, mask, draft_len, out, sm_scale=None, stream=None):
         """Attention from the drafted tokens (q [B][T][Hq][D]) to the whole cache, the window and
-        the drafted tokens their mask names; see tree_attention.  The cache is not changed."""
-        need = kb.tree_workspace_bytes(self.cfg, self.batch, q.shape[1])
-        if self.tree_workspace is None or self.tree_workspace.numel() < need:
-            self.tree_workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        the drafted tokens their mask names; see tree_attention.  The cache is not changed.  The
+        first call allocates the scratch (20 MB for every tree), so it cannot be one that is captured."""
+        if self.tree_workspace is None:
+            if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("verify allocates its scratch in its first call: call it once before a capture")
+            need = max(kb.tree_workspace_bytes(self.cfg, self.batch, T) for T in (1, 2, 4, 8, kb.MAX_DRAFT))
+            with self._on(stream):
+                self.tree_workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
         kb.tree_attention(self.cfg, self.pool, q, self.page_table, self.num_pages, self.res_k, self.res_v, self.res_len,
                           k_draft, v_draft, mask, draft_len, out, self.tree_workspace, sm_scale, self.err, stream)
 
@@ -207,7 +218,7 @@ class PagedKVCache:
             raise RuntimeError("page table full")
         if sum(fills) > len(self.free):
             raise RuntimeError("page pool exhausted")
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        with self._on(stream):
             self.n_path.copy_(torch.tensor(left, dtype=torch.int32))
             self.taken.zero_()
             while True:
@@ -228,6 +239,9 @@ class PagedKVCache:
                     self.flush(stream)
                 if not any(left):
                     break
+
+    def _on(self, stream):
+        return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
     def record(self, page: int, head: int) -> torch.Tensor:
         """Bytes of record (page, head) (a view into the pool)."""

@@ -125,3 +125,43 @@ def test_calls_on_a_side_stream():
     s.synchronize()
     assert c.check_errors() == 0 and c.res_len.tolist() == [(100 + 40) % 32] and c.num_pages.tolist() == [4]
     assert torch.equal(c.res_k[0, 0, :12], kd[0, 28:40, 0])
+
+
+def test_captured_steps_replay_after_larger_ones():
+    """Select, sparse attention and verification captured once; calls of other sizes in between."""
+    cfg = kb.Config(num_q_heads=8, num_kv_heads=2, page_tokens=32, num_boost=16)
+    c = PagedKVCache(cfg, 2, max_pages=16, pool_pages=32)
+    x = torch.randn(2, 12 * 32, 2, D, device="cuda").half()
+    c.prefill_batch(x, x)
+    q1 = torch.randn(2, 8, D, device="cuda").half()
+
+    def tree(T):
+        q, kd = torch.randn(2, T, 8, D, device="cuda").half(), torch.randn(2, T, 2, D, device="cuda").half()
+        mask = torch.from_numpy(pack_mask(tree_mask(np.random.default_rng(T), 2, T))).cuda()
+        return dict(q=q, k_draft=kd, v_draft=kd, mask=mask, draft_len=torch.full((2,), T, dtype=torch.int32, device="cuda"),
+                    out=torch.zeros(2, T, 8, D, device="cuda"))
+
+    t = tree(6)
+    few = torch.zeros(2, 8, D, device="cuda")
+
+    def step():
+        c.select(q1, 3)
+        c.attend_few(q1, few)
+        c.verify(**t)
+
+    step()
+    torch.cuda.synchronize()
+    want = few.clone(), t["out"].clone(), c.sel.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for T in (128, 1, 2, 40):
+        c.select(q1, T % 16 + 1, 0, 1)
+        c.attend_few(q1, torch.empty_like(few))
+        c.verify(**tree(T))
+        few.zero_()
+        t["out"].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert c.check_errors() == 0
+        assert torch.equal(few, want[0]) and torch.equal(t["out"], want[1]) and torch.equal(c.choices[3], want[2])

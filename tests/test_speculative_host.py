@@ -85,3 +85,30 @@ def test_refused_before_anything_changes(calls):
 def test_attend_few_needs_a_choice(calls):
     with pytest.raises(RuntimeError, match="select"):
         make().attend_few(None, None)
+
+
+def test_buffers_a_captured_graph_may_hold_are_never_replaced(monkeypatch):
+    seen = []
+    monkeypatch.setattr(kc.kb, "tree_attention", lambda *a: seen.append(a[13]))
+    monkeypatch.setattr(kc.kb, "select_pages", lambda *a: None)
+    for gqa in (1, 2, 4, 8):
+        cfg = kb.Config(num_q_heads=2 * gqa, num_kv_heads=2, page_tokens=32, num_boost=16)
+        c = kc.PagedKVCache(cfg, 3, max_pages=6, pool_pages=12, device="cpu")
+        del seen[:]
+        for T in range(1, kb.MAX_DRAFT + 1):
+            c.verify(torch.empty(3, T, 2 * gqa, 128), None, None, None, None, None)
+            assert seen[-1] is seen[0] and seen[0].numel() >= kb.tree_workspace_bytes(cfg, 3, T), T
+        first = c.select(None, 4)[0]
+        assert c.select(None, 5)[0].shape == (3, 2, 5) and c.sel is not first
+        assert c.select(None, 4)[0] is first and c.sel is first
+
+
+def test_scratch_is_not_allocated_in_a_capture(monkeypatch):
+    c = make()
+    c.device = torch.device("cuda")
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="before a capture"):
+        c.verify(torch.empty(3, 2, 4, 128), None, None, None, None, None)
+    assert c.tree_workspace is None
+    with pytest.raises(ValueError, match="at least one page"):
+        c.select(None, 0)
