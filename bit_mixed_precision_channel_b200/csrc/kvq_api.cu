@@ -390,7 +390,7 @@ kvq_status kvq_decode_attention_sparse(const kvq_config* cfg, const void* pool, 
   p.sel = sel;
   p.table_len = num_pages;
   p.table_pages = max_pages;
-  return cuda_status(launch_decode(p, cfg->num_q_heads / cfg->num_kv_heads, cfg->dtype, stream));
+  return cuda_status(launch_sparse(p, cfg->num_q_heads / cfg->num_kv_heads, cfg->dtype, stream));
 }
 
 kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q, int32_t batch,

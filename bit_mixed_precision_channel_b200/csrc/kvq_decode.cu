@@ -30,6 +30,15 @@ cudaError_t draft_launch_bf16_g2(const DecodeParams& p, cudaStream_t stream);
 cudaError_t draft_launch_bf16_g4(const DecodeParams& p, cudaStream_t stream);
 cudaError_t draft_launch_bf16_g8(const DecodeParams& p, cudaStream_t stream);
 
+cudaError_t sparse_launch_f16_g1(const DecodeParams& p, cudaStream_t stream);
+cudaError_t sparse_launch_f16_g2(const DecodeParams& p, cudaStream_t stream);
+cudaError_t sparse_launch_f16_g4(const DecodeParams& p, cudaStream_t stream);
+cudaError_t sparse_launch_f16_g8(const DecodeParams& p, cudaStream_t stream);
+cudaError_t sparse_launch_bf16_g1(const DecodeParams& p, cudaStream_t stream);
+cudaError_t sparse_launch_bf16_g2(const DecodeParams& p, cudaStream_t stream);
+cudaError_t sparse_launch_bf16_g4(const DecodeParams& p, cudaStream_t stream);
+cudaError_t sparse_launch_bf16_g8(const DecodeParams& p, cudaStream_t stream);
+
 static cudaError_t decode_occupancy(int gqa, int dtype, int kb, int P, int* n) {
   const bool bf = dtype == KVQ_BF16;
   switch (gqa) {
@@ -73,6 +82,19 @@ cudaError_t launch_decode(const DecodeParams& p, int gqa, int dtype, cudaStream_
     case 2: return bf ? decode_launch_bf16_g2(p, stream) : decode_launch_f16_g2(p, stream);
     case 4: return bf ? decode_launch_bf16_g4(p, stream) : decode_launch_f16_g4(p, stream);
     case 8: return bf ? decode_launch_bf16_g8(p, stream) : decode_launch_f16_g8(p, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// The same over chosen pages (p.sel).
+cudaError_t launch_sparse(const DecodeParams& p, int gqa, int dtype, cudaStream_t stream) {
+  if (p.batch <= 0 || p.n_ctas <= 0) return cudaSuccess;
+  const bool bf = dtype == KVQ_BF16;
+  switch (gqa) {
+    case 1: return bf ? sparse_launch_bf16_g1(p, stream) : sparse_launch_f16_g1(p, stream);
+    case 2: return bf ? sparse_launch_bf16_g2(p, stream) : sparse_launch_f16_g2(p, stream);
+    case 4: return bf ? sparse_launch_bf16_g4(p, stream) : sparse_launch_f16_g4(p, stream);
+    case 8: return bf ? sparse_launch_bf16_g8(p, stream) : sparse_launch_f16_g8(p, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -259,7 +259,8 @@ __device__ __forceinline__ void softmax_step(WarpState<NT>& st, const float (&L)
 
 // Tokens [32 grp, 32 grp + 32) of the page record `rec` (shared memory), for the lane
 // (g, qd): QK^T over planes A and B and the zero points, online softmax, then PV.
-template <typename T, int GQA, int KB, int P>
+// CENTRED: the output sums are kept near zero, see below.
+template <typename T, int GQA, int KB, int P, bool CENTRED>
 __device__ __forceinline__ void page_group(const uint8_t* rec, int grp, const LaneQ<(GQA > 4 ? 2 : 1)>& lq,
                                            const uint16_t* qs, WarpState<(GQA > 4 ? 2 : 1)>& st, int lane,
                                            int32_t* err) {
@@ -424,6 +425,29 @@ __device__ __forceinline__ void page_group(const uint8_t* rec, int grp, const La
   const float sv[4] = {s01.x, s01.y, s23.x, s23.y}, zv[4] = {z01.x, z01.y, z23.x, z23.y};
   if (__any_sync(kFull, !(fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3])) < st.vlim)))
     raise_value_exponent(st, fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3])), err);
+  if constexpr (CENTRED) {
+    // The matrix instructions round their accumulator toward zero, and the codes are never
+    // negative: over many pages that is a bias.  1.5 times the group's weights leave the sums
+    // ahead of the codes (half a code is 0.75) and join the zero points, which are summed to
+    // nearest.  Over 48 chosen pages of 64 tokens a sequence the output is then off by 1.5e-6
+    // against 64 bits instead of 6.2e-6, at 4% of the time (107 -> 111 us); the few rows of
+    // drafted tokens take no longer with it.
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float ps = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) ps = fmaf(ex2(L[u >> 1][nt][u & 1] - st.m[nt]), sv[u], ps);
+      st.zv[nt] = fmaf(1.5f, ps, st.zv[nt]);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) ps += __shfl_xor_sync(kFull, ps, off);
+      ps *= -0.75f * st.fsc;
+#pragma unroll
+      for (int mc = 0; mc < 8; ++mc) {
+        st.o[mc][nt][0] += ps;
+        st.o[mc][nt][2] += ps;
+      }
+    }
+  }
   uint32_t pb[2][NT][2];
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt)
@@ -459,13 +483,13 @@ __device__ __forceinline__ void page_group(const uint8_t* rec, int grp, const La
 // One piece of n <= 16 residual tokens staged in shared memory as K rows then V rows
 // (272-byte rows; rows n..15 hold zeros).  The PV operand carries 0.5 * p so
 // that the accumulator stays in the units of the code products.  Two bf16 parts of it hold 17
-// bits; `fine` adds a third (sparse mode, where the window is a large share of the tokens).
+// bits; FINE adds a third (over chosen pages, where the window is a large share of the tokens).
 // DRAFT: token t of the piece is drafted token t - first when that is not negative, and seen
 // by head hd if bit t - first of mk[hd >> gqa_log2] is set.
-template <typename T, int GQA, bool DRAFT>
+template <typename T, int GQA, bool DRAFT, bool FINE>
 __device__ __forceinline__ void residual_piece(const uint8_t* Kr, const uint8_t* Vr, int n, const uint16_t* qs,
                                                WarpState<(GQA > 4 ? 2 : 1)>& st, int lane, float c_log2,
-                                               int32_t* err, bool fine, const uint32_t* mk, int first,
+                                               int32_t* err, const uint32_t* mk, int first,
                                                int gqa_log2) {
   constexpr int NT = GQA > 4 ? 2 : 1;
   const int g = lane >> 2, li = lane >> 3, lr = lane & 7;
@@ -526,7 +550,7 @@ __device__ __forceinline__ void residual_piece(const uint8_t* Kr, const uint8_t*
       pb[nt][r] = movmatrix_trans(hl);
     }
 #pragma unroll 1
-  for (int part = 0; part < (kThird && fine ? 2 : 1); ++part) {
+  for (int part = 0; part < (kThird && FINE ? 2 : 1); ++part) {
 #pragma unroll
     for (int mc = 0; mc < 8; ++mc) {
       uint32_t a[4];
@@ -774,7 +798,7 @@ struct CtaShared {
 
 // Lists the next segment of this CTA's items (all threads).  One thread walks the units
 // from sh.cur; then every thread fills one descriptor and loads its page ids.
-template <int GQA, int KB, int P, bool DRAFT>
+template <int GQA, int KB, int P, bool DRAFT, bool SPARSE>
 __device__ __forceinline__ void build_segment(const DecodeParams& p, CtaShared<GQA, P, DRAFT>& sh, int hi, const Owners& ow,
                                               int tid, bool one_pass) {
   constexpr int PPC = 128 / P, GPP = P / 32;
@@ -860,7 +884,7 @@ __device__ __forceinline__ void build_segment(const DecodeParams& p, CtaShared<G
       w |= uint32_t(npg) | (uint32_t(k) << 16);
       for (int i = 0; i < npg; ++i) {
         int id;
-        if (p.sel) {  // the chosen slot of this kv head, then the page it holds
+        if constexpr (SPARSE) {  // the chosen slot of this kv head, then the page it holds
           const int slot = __ldcg(p.sel + (size_t(sp.b) * p.Hkv + sp.h) * p.max_pages + k * PPC + i);
           const int len = min(__ldcg(p.table_len + sp.b), p.table_pages);
           id = slot >= 0 && slot < len ? __ldcg(p.page_table + size_t(sp.b) * p.table_pages + slot) : -1;
@@ -1121,10 +1145,15 @@ __device__ __noinline__ void merge_partials_cta(const DecodeParams& p, int* flag
   if (warp == 3 && lane == 0) p.cnt[u] = 0u;  // ready for the next launch
 }
 
-template <typename T, int GQA, int KB, int P, bool DRAFT>
+// FORM: what the kernel attends to besides the residual window.  One template parameter, so
+// that no form pays for the others (a branch for chosen pages cost the plain form 0.5 to 1.5%).
+constexpr int kAllPages = 0, kChosenPages = 1, kDrafted = 2;  // kDrafted: all pages and drafted tokens
+
+template <typename T, int GQA, int KB, int P, int FORM>
 __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
     decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int NT = GQA > 4 ? 2 : 1;
+  constexpr bool DRAFT = FORM == kDrafted, SPARSE = FORM == kChosenPages;
   using R = Rec<P, KB>;
   using S = Smem<GQA, P, KB>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -1273,7 +1302,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
   {
     locate(lo);
     while (true) {
-      build_segment<GQA, KB, P, DRAFT>(p, sh, hi, ow, tid, one_pass);
+      build_segment<GQA, KB, P, DRAFT, SPARSE>(p, sh, hi, ow, tid, one_pass);
       const int nseg = sh.nseg;
       if (warp == 0)
         for (int t = 0; t < min(kStages, nseg); ++t) issue_item<GQA, KB, P, DRAFT>(p, sh, smem, x + t, t, policy, lane);
@@ -1337,11 +1366,11 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
         if (ok) {
           if (!(d.w & kDescRes)) {
             const int pw = (32 * warp) / P, grp = ((32 * warp) % P) / 32;
-            if (pw < n) page_group<T, GQA, KB, P>(sb + pw * R::record, grp, lq, qs, st, lane, p.err);
+            if (pw < n) page_group<T, GQA, KB, P, SPARSE || DRAFT>(sb + pw * R::record, grp, lq, qs, st, lane, p.err);
           } else if (int(d.w >> 16) % 4 == warp) {
-            residual_piece<T, GQA, DRAFT>(sb, sb + kPieceTokens * kResRowBytes, n, qs, st, lane, p.c_log2, p.err,
-                                          DRAFT || p.sel != nullptr, sh.mk[DRAFT ? stg : 0], DRAFT ? sh.first[stg] : 0,
-                                          p.gqa_log2);
+            residual_piece<T, GQA, DRAFT, DRAFT || SPARSE>(sb, sb + kPieceTokens * kResRowBytes, n, qs, st, lane, p.c_log2,
+                                                           p.err, sh.mk[DRAFT ? stg : 0], DRAFT ? sh.first[stg] : 0,
+                                                           p.gqa_log2);
           }
         }
         // release the stage; the last warp to release it refills it with item xi + kStages
@@ -1461,10 +1490,10 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
 
 // ---------------------------------------------------------------- per-instantiation host side
 
-template <typename T, int GQA, int KB, int P, bool DRAFT>
+template <typename T, int GQA, int KB, int P, int FORM>
 cudaError_t prepare_decode() {
   static int seen[64];
-  return ensure_dynamic_smem(decode_kernel<T, GQA, KB, P, DRAFT>, int(Smem<GQA, P, KB>::bytes), seen);
+  return ensure_dynamic_smem(decode_kernel<T, GQA, KB, P, FORM>, int(Smem<GQA, P, KB>::bytes), seen);
 }
 
 // Calls f.template operator()<KB, P>() for one (kb, P).
@@ -1493,23 +1522,23 @@ struct DecodeOcc {
   int* n;
   template <int KB, int P>
   cudaError_t operator()() {
-    cudaError_t e = prepare_decode<T, GQA, KB, P, false>();
+    cudaError_t e = prepare_decode<T, GQA, KB, P, kAllPages>();
     if (e != cudaSuccess) return e;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, decode_kernel<T, GQA, KB, P, false>, kDecodeThreads,
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, decode_kernel<T, GQA, KB, P, kAllPages>, kDecodeThreads,
                                                          Smem<GQA, P, KB>::bytes);
   }
 };
 
-template <typename T, int GQA, bool DRAFT>
+template <typename T, int GQA, int FORM>
 struct DecodeRun {
   const DecodeParams& p;
   cudaStream_t stream;
   template <int KB, int P>
   cudaError_t operator()() {
     if (p.L.record != Rec<P, KB>::record || p.L.payload != Rec<P, KB>::payload) return cudaErrorInvalidValue;
-    cudaError_t e = prepare_decode<T, GQA, KB, P, DRAFT>();
+    cudaError_t e = prepare_decode<T, GQA, KB, P, FORM>();
     if (e != cudaSuccess) return e;
-    return launch_pdl(decode_kernel<T, GQA, KB, P, DRAFT>, dim3(p.n_ctas), dim3(kDecodeThreads), Smem<GQA, P, KB>::bytes,
+    return launch_pdl(decode_kernel<T, GQA, KB, P, FORM>, dim3(p.n_ctas), dim3(kDecodeThreads), Smem<GQA, P, KB>::bytes,
                       stream, p);
   }
 };
@@ -1520,12 +1549,16 @@ struct DecodeRun {
     return dispatch_kb_p(kb, P, DecodeOcc<T, GQA>{n});                                          \
   }                                                                                             \
   cudaError_t decode_launch_##NAME(const DecodeParams& p, cudaStream_t stream) {               \
-    return dispatch_kb_p(p.KB, p.P, DecodeRun<T, GQA, false>{p, stream});                       \
+    return dispatch_kb_p(p.KB, p.P, DecodeRun<T, GQA, kAllPages>{p, stream});                       \
   }
-// ... and one the launch for drafted tokens.
+// ... and others the launches for chosen pages and for drafted tokens.
+#define KVQ_SPARSE_INSTANCE(NAME, T, GQA)                                                       \
+  cudaError_t sparse_launch_##NAME(const DecodeParams& p, cudaStream_t stream) {                \
+    return dispatch_kb_p(p.KB, p.P, DecodeRun<T, GQA, kChosenPages>{p, stream});                \
+  }
 #define KVQ_DRAFT_INSTANCE(NAME, T, GQA)                                                        \
   cudaError_t draft_launch_##NAME(const DecodeParams& p, cudaStream_t stream) {                 \
-    return dispatch_kb_p(p.KB, p.P, DecodeRun<T, GQA, true>{p, stream});                        \
+    return dispatch_kb_p(p.KB, p.P, DecodeRun<T, GQA, kDrafted>{p, stream});                        \
   }
 
 }  // namespace kvq

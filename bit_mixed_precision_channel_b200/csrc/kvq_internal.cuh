@@ -412,6 +412,7 @@ cudaError_t launch_tree(const TreeParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_flush_commit(int32_t* res_len, const int32_t* new_page, int32_t* page_table, int max_pages,
                                 int32_t* num_pages, long long pool_pages, int batch, int P, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams& p, int gqa, int dtype, cudaStream_t stream);
+cudaError_t launch_sparse(const DecodeParams& p, int gqa, int dtype, cudaStream_t stream);
 cudaError_t launch_draft(const DecodeParams& p, int rows, int dtype, cudaStream_t stream);
 cudaError_t launch_prefill(const void* q, const void* k, const void* v, int L, int Hq, int Hkv, float sm_scale,
                            int dtype, float* out, float* lse, float* score, cudaStream_t stream);

@@ -418,7 +418,8 @@ KVQ_API kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int
  * outside [0, num_pages[b]) sets KVQ_DEV_ERR_PAGE_RANGE, n_sel[b] outside [0, max_sel]
  * KVQ_DEV_ERR_LENGTH.  Everything else (q, out, workspace of
  * kvq_decode_workspace_bytes(cfg, batch, max_pages) bytes with its zero-counter contract,
- * precision, empty sequences, errors) as for kvq_decode_attention, on the same kernel. */
+ * precision, empty sequences, errors) as for kvq_decode_attention; the sums over the values
+ * are kept near zero on the way, so they are off by less over long choices. */
 KVQ_API kvq_status kvq_decode_attention_sparse(const kvq_config* cfg, const void* pool, int64_t pool_pages,
                                                const void* q, int32_t batch, const int32_t* page_table,
                                                int32_t max_pages, const int32_t* num_pages, const int32_t* sel,
