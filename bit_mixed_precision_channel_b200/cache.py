@@ -41,11 +41,10 @@ class PagedKVCache:
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.new_page = torch.full((batch,), -1, dtype=torch.int32, device=self.device)
         self.counters = torch.zeros(batch, dtype=torch.int32, device=self.device)  # append_flush arrivals
-        # speculative decoding: the last choice of pages and the buffer of every size asked for, the
+        # speculative decoding: the last choice of pages and the buffers of every size asked for, the
         # accepted lengths, the tree's scratch.  Captured graphs may hold these buffers: none is replaced.
-        self.sel = None
+        self.sel = self.n_sel = None
         self.choices = {}
-        self.n_sel = torch.zeros(batch, dtype=torch.int32, device=self.device)
         self.n_path = torch.zeros(batch, dtype=torch.int32, device=self.device)
         self.taken = torch.zeros(batch, dtype=torch.int32, device=self.device)
         self.tree_workspace = None
@@ -178,12 +177,14 @@ class PagedKVCache:
             if n_select < 1:
                 raise ValueError(f"n_select is {n_select}: at least one page")
             with self._on(stream):
-                self.choices[n_select] = torch.empty(self.batch, self.cfg.num_kv_heads, n_select, dtype=torch.int32,
-                                                     device=self.device)
-        self.sel = self.choices[n_select]
-        kb.select_pages(self.cfg, self.pool, q, self.page_table, self.num_pages, self.sel, self.n_sel, n_first, n_recent,
-                        self.err, stream)
-        return self.sel, self.n_sel
+                self.choices[n_select] = (
+                    torch.empty(self.batch, self.cfg.num_kv_heads, n_select, dtype=torch.int32, device=self.device),
+                    torch.empty(self.batch, dtype=torch.int32, device=self.device))
+        sel, n_sel = self.choices[n_select]
+        kb.select_pages(self.cfg, self.pool, q, self.page_table, self.num_pages, sel, n_sel, n_first, n_recent, self.err,
+                        stream)
+        self.sel, self.n_sel = sel, n_sel
+        return sel, n_sel
 
     def attend_few(self, q, out, sm_scale=None, stream=None):
         """Decode attention over the pages of the last `select` and the window."""

@@ -164,4 +164,27 @@ def test_captured_steps_replay_after_larger_ones():
         g.replay()
         torch.cuda.synchronize()
         assert c.check_errors() == 0
-        assert torch.equal(few, want[0]) and torch.equal(t["out"], want[1]) and torch.equal(c.choices[3], want[2])
+        assert torch.equal(few, want[0]) and torch.equal(t["out"], want[1]) and torch.equal(c.choices[3][0], want[2])
+
+
+def test_a_captured_draft_step_keeps_its_choice():
+    """A graph of attend_few alone goes on with the choice it was captured with, whatever is chosen after."""
+    cfg = kb.Config(num_q_heads=8, num_kv_heads=2, page_tokens=32, num_boost=16)
+    c = PagedKVCache(cfg, 2, max_pages=16, pool_pages=32)
+    x = torch.randn(2, 12 * 32, 2, D, device="cuda").half()
+    c.prefill_batch(x, x)
+    q = torch.randn(2, 8, D, device="cuda").half()
+    out = torch.zeros(2, 8, D, device="cuda")
+    c.select(q, 3)
+    c.attend_few(q, out)
+    torch.cuda.synchronize()
+    want = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.attend_few(q, out)
+    c.select(-q, 9)
+    c.attend_few(q, torch.empty_like(out))
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert c.check_errors() == 0 and torch.equal(out, want)

@@ -98,9 +98,11 @@ def test_buffers_a_captured_graph_may_hold_are_never_replaced(monkeypatch):
         for T in range(1, kb.MAX_DRAFT + 1):
             c.verify(torch.empty(3, T, 2 * gqa, 128), None, None, None, None, None)
             assert seen[-1] is seen[0] and seen[0].numel() >= kb.tree_workspace_bytes(cfg, 3, T), T
-        first = c.select(None, 4)[0]
-        assert c.select(None, 5)[0].shape == (3, 2, 5) and c.sel is not first
-        assert c.select(None, 4)[0] is first and c.sel is first
+        first = c.select(None, 4)
+        other = c.select(None, 5)
+        assert other[0].shape == (3, 2, 5) and c.sel is other[0] and c.n_sel is other[1] is not first[1]
+        again = c.select(None, 4)
+        assert again[0] is first[0] is c.sel and again[1] is first[1] is c.n_sel
 
 
 def test_scratch_is_not_allocated_in_a_capture(monkeypatch):
@@ -112,3 +114,16 @@ def test_scratch_is_not_allocated_in_a_capture(monkeypatch):
     assert c.tree_workspace is None
     with pytest.raises(ValueError, match="at least one page"):
         c.select(None, 0)
+
+
+def test_a_refused_choice_leaves_the_last_one(monkeypatch):
+    def select_pages(cfg, pool, q, table, num, sel, n_sel, n_first, n_recent, err, stream):
+        if n_first + n_recent > sel.shape[2]:
+            raise kb.KVQError("kvq_select_pages", 1)
+
+    monkeypatch.setattr(kc.kb, "select_pages", select_pages)
+    c = make()
+    first = c.select(None, 4)
+    with pytest.raises(kb.KVQError):
+        c.select(None, 1)
+    assert c.sel is first[0] and c.n_sel is first[1]
