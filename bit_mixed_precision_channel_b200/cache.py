@@ -45,6 +45,8 @@ class PagedKVCache:
         # accepted lengths, the tree's scratch.  Captured graphs may hold these buffers: none is replaced.
         self.sel = self.n_sel = None
         self.choices = {}
+        self.grown = 0         # calls that may have appended pages
+        self.grown_at_sel = 0  # ... when the last choice was made
         self.n_path = torch.zeros(batch, dtype=torch.int32, device=self.device)
         self.taken = torch.zeros(batch, dtype=torch.int32, device=self.device)
         self.tree_workspace = None
@@ -73,6 +75,7 @@ class PagedKVCache:
         if len(self.host_pages[b]) + n_full > self.max_pages:
             raise RuntimeError("page table full")
         pages = self.take_pages(n_full)
+        self.grown += bool(n_full)
         if n_full:
             dst = torch.tensor(pages, dtype=torch.int32, device=self.device)
             kb.quantize_pages(self.cfg, kb.Source.token_major(k, self.cfg), kb.Source.token_major(v, self.cfg),
@@ -96,6 +99,7 @@ class PagedKVCache:
         assert B == self.batch and L % P == 0 and k.is_contiguous() and v.is_contiguous()
         n = L // P
         pages = self.take_pages(B * n)
+        self.grown += 1
         dst = torch.tensor(pages, dtype=torch.int32, device=self.device)
         flat_k, flat_v = k.view(B * L, *k.shape[2:]), v.view(B * L, *v.shape[2:])
         kb.quantize_pages(self.cfg, kb.Source.token_major(flat_k, self.cfg), kb.Source.token_major(flat_v, self.cfg),
@@ -127,6 +131,7 @@ class PagedKVCache:
         P = self.cfg.page_tokens
         for b in range(self.batch):
             self.host_res_len[b] += 1
+        self.grown += bool(flushing)
         for b in flushing:
             self.host_pages[b].append(self.host_new_page[b])
             self.host_res_len[b] = 0
@@ -136,11 +141,13 @@ class PagedKVCache:
         kb.append_token(self.cfg, k_new, v_new, self.res_k, self.res_v, self.res_len, self.err, stream)
 
     def flush(self, stream=None):
+        self.grown += max(self.host_new_page, default=-1) >= 0
         kb.flush_residual(self.cfg, self.res_k, self.res_v, self.res_len, self.new_page, self.page_table,
                           self.num_pages, self.pool, self.err, stream)
 
     def append_flush(self, k_new, v_new, stream=None):
         """append then flush, in one launch."""
+        self.grown += max(self.host_new_page, default=-1) >= 0
         kb.append_flush(self.cfg, k_new, v_new, self.res_k, self.res_v, self.res_len, self.new_page,
                         self.page_table, self.num_pages, self.pool, self.counters, self.err, stream)
 
@@ -171,8 +178,9 @@ class PagedKVCache:
     def select(self, q, n_select: int, n_first: int = 1, n_recent: int = 1, stream=None):
         """Chooses the n_select pages of every (sequence, KV head) whose stored key ranges
         allow q the largest logits (the first n_first and the last n_recent always): fills
-        and returns self.sel [B][Hkv][n_select] and self.n_sel [B].  A choice stays valid
-        while pages are only appended."""
+        and returns self.sel [B][Hkv][n_select] and self.n_sel [B].  A choice holds until a
+        window is flushed: the page then holds tokens that the choice does not list, so
+        attend_few asks for a new one."""
         if n_select not in self.choices:
             if n_select < 1:
                 raise ValueError(f"n_select is {n_select}: at least one page")
@@ -184,12 +192,17 @@ class PagedKVCache:
         kb.select_pages(self.cfg, self.pool, q, self.page_table, self.num_pages, sel, n_sel, n_first, n_recent, self.err,
                         stream)
         self.sel, self.n_sel = sel, n_sel
+        self.grown_at_sel = self.grown
         return sel, n_sel
 
     def attend_few(self, q, out, sm_scale=None, stream=None):
-        """Decode attention over the pages of the last `select` and the window."""
+        """Decode attention over the pages of the last `select` and the window.  Refused once
+        pages were appended since (a graph that holds this call has to hold its `select` too,
+        if it is replayed across a flush)."""
         if self.sel is None:
             raise RuntimeError("attend_few needs a choice of pages: call select first")
+        if self.grown_at_sel != self.grown:
+            raise RuntimeError("pages were appended since the last choice, which leaves their tokens out: call select again")
         kb.decode_attention_sparse(self.cfg, self.pool, q, self.page_table, self.num_pages, self.sel, self.n_sel,
                                    self.res_k, self.res_v, self.res_len, out, self.workspace, sm_scale, self.err, stream)
 
