@@ -33,8 +33,9 @@
 //  * the value scale is folded into the probability, P = p * sV as a high and a low fp16
 //    part, so the value operand is the 2-bit codes themselves, centred (code - 1.5) so that
 //    sums do not cancel against the zero points; sum p (z + 1.5 sV) is added in fp32.
-//    The running reference M covers the largest p * sV of a tile, so P stays inside fp16
-//    whatever the value scales are;
+//    The running reference M covers the largest logit of a tile with its largest sV (of raw
+//    bf16 tokens the largest p * sV that the row sees), so P stays inside fp16 whatever the
+//    value scales are;
 //  * window and drafted tokens go through the same products: K / 2 and V * 2^-e_t in fp16,
 //    with 2^e_t (bf16 only; the token's largest value) in the place of the value scale.
 #pragma once
@@ -54,9 +55,15 @@ constexpr int kIssuer = kSoftWarps + kDeqWarps, kProducer = kIssuer + 1, kMover 
 constexpr int kThreads = 896;  // 7 warpgroups: two of softmax, four of dequant, one of single warps
 // Registers a thread: at launch, then by role (setmaxnreg): 2 x 112 + 4 x 56 + 56 = 7 x 72,
 // so the split draws on exactly what the block was launched with.  The shared memory leaves
-// next to no L1, so a register spilled in a role's loop costs an L2 access.
-constexpr int kRegsLaunch = 72, kRegsSoft = 112, kRegsDeq = 56, kRegsRest = 56;
-static_assert(2 * kRegsSoft + 4 * kRegsDeq + kRegsRest <= 7 * kRegsLaunch, "register split");
+// next to no L1, so a register spilled in a role's loop costs an L2 access.  bf16, whose dequant
+// warps also convert the scales: 2 x 104 + 4 x 64 + 40 (ragged 32 x 8192 of 61 nodes, 32 boosted
+// channels: 672 against 700 us; fp16 16 x 4096 of 32 nodes: 113.2 against 111.8).
+constexpr int kRegsLaunch = 72;
+template <bool BF>
+struct Regs {
+  static constexpr int soft = BF ? 104 : 112, deq = BF ? 64 : 56, rest = BF ? 40 : 56;
+  static_assert(2 * soft + 4 * deq + rest <= 7 * kRegsLaunch, "register split");
+};
 // (two where every channel may be boosted: the moves take the third's place)
 constexpr int rec_stages(int KB) { return KB == 8 ? 2 : 3; }
 // The tensor cores round their fp32 accumulator toward zero: 16 products a tile shrink a long
@@ -193,6 +200,9 @@ __device__ __forceinline__ uint32_t scaled_h2(uint32_t x, float f, __nv_bfloat16
 __device__ __forceinline__ uint32_t half_of(uint32_t x) {  // x / 2 of an fp16 pair
   return h2_as_u32(__hmul2(u32_as_h2(x), __float2half2_rn(0.5f)));
 }
+
+// The least integer n >= -20 with a value scale below 2^n.
+__device__ __forceinline__ float scale_log2(float s) { return float(max(-20, int((__float_as_uint(s) >> 23) & 0xff) - 126)); }
 
 // Not zero if an element of the fp16 pair is no finite number: an exponent of ones carries
 // into the place of the sign.
@@ -350,10 +360,10 @@ struct Shared {
       p_full[2], pv_done[2], q_full;
   uint32_t tmem;
   int abort;
-  // value scale s (raw tiles: 2^e_t / 2) and zero point + 1.5 s of two tokens {s, s', z, z'}
+  // of two tokens {s, s', z, z'}: value scale (raw tiles: 2^e_t / 2), zero point + 1.5 s (raw
+  // tiles have none: 0, in bf16 scale_log2(s))
   float4 sz[3][64];
   float smax[3][4];                     // largest value scale of a page tile's groups
-  float xs[3][kDeqWarps];               // the same of a raw tile, by the warp that wrote it
   Line line;
   __align__(16) Moves moves[KB > 0 ? kRecStages : 1][KB > 0 ? 4 : 1];  // [stage][page of the tile]
 };
@@ -643,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   if (idle) {
     // nothing to do
   } else if (warp >= kIssuer) {
-    regs_dec<kRegsRest>();
+    regs_dec<Regs<BF>::rest>();
     if (warp == kProducer) {
     // ------------------------------------------------------------ producer
     const uint64_t policy = l2_evict_first_policy();
@@ -788,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
   } else if (warp >= kSoftWarps) {
     // ------------------------------------------------------------ dequantization
-    regs_dec<kRegsDeq>();
+    regs_dec<Regs<BF>::deq>();
     const int dw = warp - kSoftWarps, g = dw >> 2, half = (dw >> 1) & 1, a = dw & 1;
     const int pg = g >> p.gpp_log2, gp = g - (pg << p.gpp_log2);  // page of the tile, group of the page
     int it = 0, n = 0;  // tiles whose keys are written; page tiles among them
@@ -885,7 +895,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         // the values: what is no number is zero (a probability of zero has to stay zero), and
         // bf16 is brought below 2 by the token's power of two
         rows(p.res_v, p.v_draft, x);
-        float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int xi = x0 + 2 * i;
@@ -904,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             }
 #pragma unroll
             for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-            const int e2 = max(-90, min(100, int((__float_as_uint(m) >> 23) & 0xff) - 127));
+            const int e2 = max(-90, min(126, int((__float_as_uint(m) >> 23) & 0xff) - 127));  // (below 4 at 2^127)
             s *= pow2i(e2);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = scaled_h2(v[e], pow2i(-e2), T());
@@ -914,12 +923,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const int t = t0 + 2 * i;
             float* sz = reinterpret_cast<float*>(sh.sz[v3]) + 4 * (t >> 1) + (t & 1);
             sz[0] = s;
-            sz[2] = 0.0f;
+            sz[2] = BF ? scale_log2(s) : 0.0f;
           }
-          top = fmaxf(top, s);
         }
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
-        if (lane == 0) sh.xs[v3][dw] = top;
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_full);
@@ -940,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     if (BF && badz) flag_error(p.err, KVQ_DEV_ERR_RANGE);
   } else {
     // ------------------------------------------------------------ softmax
-    regs_inc<kRegsSoft>();
+    regs_inc<Regs<BF>::soft>();
     const int row0 = 32 * (warp & 3) + 16 * (warp >> 2), quad = lane & 3;  // of the warp's rows the first; the lane's place
     const int row = row0 + (lane >> 2);                                    // ... and row + 8
     const uint32_t at = uint32_t(row0) << 16;                              // the warp's tensor-memory lanes
@@ -1128,12 +1134,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           }
           tc::wait_st();
         }
-        // first pass: the rows' largest logits (S is read again for the second)
+        // first pass: the rows' largest logits (S is read again for the second).  Raw bf16 tokens
+        // have scales of any size, hidden ones too: there each logit counts with its own token's
+        // scale, in the units of M, so that what a row does not see cannot move its reference
         float mx[2] = {-INFINITY, -INFINITY};
+        const float4* sz = &sh.sz[v3][quad];
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {
           uint32_t x[16];
           ld32(tS + 32 * g, x);
+          if (BF && raw) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float4 v = sz[16 * g + 4 * c];
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                mx[r] = fmaxf(mx[r], fmaxf(fmaf(__uint_as_float(x[4 * c + 2 * r]), cl[r], v.z),
+                                           fmaf(__uint_as_float(x[4 * c + 2 * r + 1]), cl[r], v.w)));
+            }
+            continue;
+          }
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             float m = -INFINITY;
@@ -1143,20 +1163,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             mx[r] = fmaxf(mx[r], m + __shfl_sync(kFull, __uint_as_float(zr[r]), (lane & ~3) + g));
           }
         }
-        float sm;
-        if (!raw) {
-          sm = fmaxf(fmaxf(sh.smax[v3][0], sh.smax[v3][1]), fmaxf(sh.smax[v3][2], sh.smax[v3][3]));
-        } else {
-          sm = sh.xs[v3][0];
-#pragma unroll
-          for (int j = 1; j < kDeqWarps; ++j) sm = fmaxf(sm, sh.xs[v3][j]);
-        }
-        // sm < 2^lg; probabilities are carried as 2^(x - M + 7), so p * s starts below 2^7
-        const float lg = float(max(-20, int((__float_as_uint(sm) >> 23) & 0xff) - 126));
+        // probabilities are carried as 2^(x - M + 7), so p * s starts below 2^7 (raw fp16: s = 1/2)
+        const float lg = raw ? 0.0f
+                             : scale_log2(fmaxf(fmaxf(sh.smax[v3][0], sh.smax[v3][1]), fmaxf(sh.smax[v3][2], sh.smax[v3][3])));
         float alpha[2], nm[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float top = fmaf(quad_max(mx[r]), cl[r], lg);
+          const float top = BF && raw ? quad_max(mx[r]) : fmaf(quad_max(mx[r]), cl[r], lg);
           alpha[r] = 1.0f;
           if (top > M[r] + 8.0f) {  // p * s could pass 2^15
             alpha[r] = ex2(M[r] - top);  // M = -inf: 0
@@ -1168,7 +1181,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           nm[r] = M[r] == -INFINITY ? 0.0f : 7.0f - M[r];
         }
         // second pass
-        const float4* sz = &sh.sz[v3][quad];
         uint64_t tl[2] = {0ull, 0ull}, tz[2] = {0ull, 0ull};
         const uint64_t cl2[2] = {f2(cl[0], cl[0]), f2(cl[1], cl[1])};
 #pragma unroll 1
@@ -1185,7 +1197,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         for (int r = 0; r < 2; ++r) {
           const float2 a = f2_get(tl[r]), z = f2_get(tz[r]);
           l[r] += a.x + a.y;
-          zs[r] += z.x + z.y;
+          if (!(BF && raw)) zs[r] += z.x + z.y;
         }
         const bool flush = run > 0 && run % kFlush == 0;
         if (flush && run == kFlush) {  // the rows of the unit before have left

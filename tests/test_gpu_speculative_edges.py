@@ -1,0 +1,87 @@
+"""What a mask hides, values and queries at the ends of their ranges, and inputs that have to raise
+a device flag, for the calls of speculative decoding."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from bit_mixed_precision_channel_b200 import binding as kb
+from bit_mixed_precision_channel_b200 import synthetic as syn
+
+from _kv import to_dev
+from _spec import Cache, D
+from test_gpu_select import run_select, sparse
+from test_gpu_tree import call, check, make
+
+pytestmark = pytest.mark.gpu
+
+
+def bits(x, dtype):
+    return syn.to_bits(np.float32([x]), dtype)[0]
+
+
+# ---------------------------------------------------------------- hidden and far values
+
+
+@pytest.mark.parametrize("gqa", [1, 4, 8])
+@pytest.mark.parametrize("dtype,value", [(kb.F16, 6e4), (kb.BF16, 1e4), (kb.BF16, 2.0 ** 60), (kb.BF16, 2.0 ** 120),
+                                         (kb.BF16, 3.3e38)])
+def test_a_token_no_row_sees_may_hold_any_number(dtype, value, gqa):
+    """A hidden token of finite, large values is no part of any row, nor of the precision it is carried with."""
+    cfg = kb.Config(num_q_heads=gqa, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=dtype)
+    sees = np.tril(np.ones((2, 6, 6), bool))
+    sees[:, :, 3] = False
+    c = make(cfg, [2, 1], [4, 0], 6, [6, 5], seed=2, sees=sees)
+    sign = np.where(np.arange(D) % 3 == 0, -1.0, 1.0).astype(np.float32)
+    c.k[:, 3] = c.v[:, 3] = syn.to_bits(np.float32(value) * sign, dtype)
+    c.t["k_draft"], c.t["v_draft"] = to_dev(c.k, dtype), to_dev(c.v, dtype)
+    call(c)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    check(c)
+
+
+@pytest.mark.parametrize("some", [0, 5])
+def test_a_token_one_row_sees_does_not_reach_the_others(some):
+    """Row `some` alone sees the token of large values: the others' results are as without it."""
+    cfg = kb.Config(num_q_heads=8, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=kb.BF16)
+    sees = np.tril(np.ones((1, 6, 6), bool))
+    sees[:, :, 3] = False
+    sees[:, some, 3] = True
+    c = make(cfg, [3], [9], 6, [6], seed=8, sees=sees)
+    c.v[:, 3] = bits(2.0 ** 70, kb.BF16)
+    c.t["v_draft"] = to_dev(c.v, kb.BF16)
+    call(c)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    check(c, rows=[i for i in range(6) if i != some])
+
+
+def test_a_far_token_of_large_values_leaves_the_near_ones_their_bits():
+    """A drafted token every row sees, of weight exp(-28) and values 2^30: 2^-10 of the result.
+
+    Tolerance: a weight off by a factor within 1 +- e moves the mean by at most e sum p |v - o|, with e as in
+    _spec.py; sums of products are off by 2^-17 sum p max|v|; a weight times its value scale is carried to 2^-31
+    of the largest (a high and a low fp16 part, the largest above 2^6, an absolute step of 2^-25)."""
+    cfg = kb.Config(num_q_heads=8, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=kb.BF16)
+    c = make(cfg, [0], [20], 4, [4], seed=30, chain=True)
+    q0 = syn.from_bits(c.q[0, 0, 0], kb.BF16).astype(np.float64)
+    c.q[:] = c.q[0, 0, 0]
+    c.k[0, 0] = syn.to_bits((-28.0 * np.sqrt(D) / (q0 @ q0) * q0).astype(np.float32), kb.BF16)
+    c.v[0, 0] = bits(2.0 ** 30, kb.BF16)
+    c.t.update(q=to_dev(c.q, kb.BF16), k_draft=to_dev(c.k, kb.BF16), v_draft=to_dev(c.v, kb.BF16))
+    call(c)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    K, V = c.rows(0, 0)
+    for i in range(4):
+        Ki = np.concatenate([K, syn.from_bits(c.k[0, :i + 1, 0], kb.BF16).astype(np.float64)])
+        Vi = np.concatenate([V, syn.from_bits(c.v[0, :i + 1, 0], kb.BF16).astype(np.float64)])
+        z = Ki @ q0 / np.sqrt(D)
+        p = np.exp(z - z.max())
+        p /= p.sum()
+        o, top = p @ Vi, np.abs(Vi).max(1)
+        e = 2.0 ** -16 * (np.abs(Ki) @ np.abs(q0)).max() / np.sqrt(D) + 2.0 ** -20
+        tol = 2 * e * (p[:, None] * np.abs(Vi - o)).sum(0).max() + 2.0 ** -17 * (p @ top) + 2.0 ** -30 * len(p) * (p * top).max()
+        got = c.out[0, i].cpu().numpy()
+        assert np.isfinite(got).all() and np.abs(got - o).max() <= tol < 0.01
