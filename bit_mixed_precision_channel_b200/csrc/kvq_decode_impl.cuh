@@ -483,7 +483,8 @@ __device__ __forceinline__ void page_group(const uint8_t* rec, int grp, const La
 // One piece of n <= 16 residual tokens staged in shared memory as K rows then V rows
 // (272-byte rows; rows n..15 hold zeros).  The PV operand carries 0.5 * p so
 // that the accumulator stays in the units of the code products.  Two bf16 parts of it hold 17
-// bits; FINE adds a third (over chosen pages, where the window is a large share of the tokens).
+// bits; FINE adds a third (over chosen pages, where the window is a large share of the tokens) and
+// flags logits that are no finite number, one of minus infinity too.
 // DRAFT: token t of the piece is drafted token t - first when that is not negative, and seen
 // by head hd if bit t - first of mk[hd >> gqa_log2] is set.
 template <typename T, int GQA, bool DRAFT, bool FINE>
@@ -514,22 +515,20 @@ __device__ __forceinline__ void residual_piece(const uint8_t* Kr, const uint8_t*
     }
   }
   float L[1][NT][2];
+  bool bad = false;  // a logit that is no finite number, before a maximum hides it
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt) {
+    const uint32_t see = DRAFT ? mk[((lane & 3) + 4 * nt) >> gqa_log2] : 0u;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-      L[0][nt][r] = (g + 8 * r) < n ? (acc[nt][2 * r] + acc[nt][2 * r + 1]) * c_log2 : -INFINITY;
-  if constexpr (DRAFT) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const uint32_t see = mk[((lane & 3) + 4 * nt) >> gqa_log2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int d = g + 8 * r - first;
-        if (d >= 0 && !((see >> (d & 31)) & 1u)) L[0][nt][r] = -INFINITY;
-      }
+    for (int r = 0; r < 2; ++r) {
+      const float x = (acc[nt][2 * r] + acc[nt][2 * r + 1]) * c_log2;
+      const int d = g + 8 * r - first;
+      const bool in = (g + 8 * r) < n && (!DRAFT || d < 0 || ((see >> (d & 31)) & 1u));
+      if (FINE) bad |= in && !(fabsf(x) < INFINITY);
+      L[0][nt][r] = in ? x : -INFINITY;
     }
   }
+  if (FINE && bad) flag_error(err, KVQ_DEV_ERR_RANGE);
   softmax_step<NT, 1>(st, L, err);
   constexpr bool kThird = std::is_same<T, __nv_bfloat16>::value;
   uint32_t pb[NT][2];
@@ -1420,6 +1419,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
           float* outu = out_base<GQA, DRAFT>(p, d.b, d.h);
           const int rows = out_rows<GQA, DRAFT>(p, d.b);
           float* part_me = p.part + (size_t(owner) + u) * GQA * kPartStride;
+          float chk = 0.0f;  // 0, or no number once a sum is none: a value that is none reaches rows that do not see it
           for (int e = tid; e < GQA * kHeadDim; e += kDecodeThreads) {
             const int h = e >> 7, ch = e & 127;
             float M = -INFINITY;
@@ -1434,6 +1434,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
                 O += f * (kCodeScale * sO[(w * GQA + h) * kHeadDim + ch] + sh.zv[w][h]);
               }
             }
+            if ((DRAFT || SPARSE) && (!DRAFT || h < rows)) chk = fmaf(O, 0.0f, chk);
             if (sole) {
               if (!DRAFT || h < rows) outu[out_row<DRAFT>(p, h) + ch] = Ls > 0.0f ? O / Ls : 0.0f;
             } else {
@@ -1445,6 +1446,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
               }
             }
           }
+          if ((DRAFT || SPARSE) && chk != 0.0f) flag_error(p.err, KVQ_DEV_ERR_RANGE);
           if (!sole) {
             // ---- split merge: the last of the contributors i0..i1 merges their partials.
             // The barrier orders every thread's partial writes before the counter update,

@@ -458,9 +458,9 @@ KVQ_API size_t kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t batch, in
  * kvq_decode_attention, on its kernel.  With more, half of a dequantized key (and q * 2^-e,
  * e as there) enters as fp16, the codes times their scale as a high and a low part, the
  * probabilities times their value scale as a high and a low part, sums and softmax
- * statistics in fp32.  A group of keys that spans more than 130944, a key or zero point
- * above 131008 in magnitude (bf16), and whatever a row sees that is not finite set
- * KVQ_DEV_ERR_RANGE (the output is then undefined). */
+ * statistics in fp32; a group of keys that spans more than 130944, and a key or zero point
+ * above 131008 in magnitude (bf16), set KVQ_DEV_ERR_RANGE.  With any number of rows, so does
+ * whatever a row sees that is not finite (the output is then undefined). */
 KVQ_API kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
                                       int32_t n_draft, int32_t batch, const int32_t* page_table,
                                       int32_t max_pages, const int32_t* num_pages, const void* res_k,

@@ -85,3 +85,35 @@ def test_a_far_token_of_large_values_leaves_the_near_ones_their_bits():
         tol = 2 * e * (p[:, None] * np.abs(Vi - o)).sum(0).max() + 2.0 ** -17 * (p @ top) + 2.0 ** -30 * len(p) * (p * top).max()
         got = c.out[0, i].cpu().numpy()
         assert np.isfinite(got).all() and np.abs(got - o).max() <= tol < 0.01
+
+
+# ---------------------------------------------------------------- values and keys that are no finite number
+
+
+@pytest.mark.parametrize("T,gqa", [(2, 4), (6, 1), (3, 4)])
+@pytest.mark.parametrize("dtype", [kb.F16, kb.BF16])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_values_that_are_no_number_are_flagged_if_a_row_sees_them(value, dtype, T, gqa):
+    cfg = kb.Config(num_q_heads=gqa, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=dtype)
+    c = make(cfg, [2], [4], T, [T], seed=3, sees=np.eye(T, dtype=bool)[None])
+    c.t["v_draft"][:, 1, :, 9] = value  # a sibling of token 0, which does not see it
+    call(c)
+    torch.cuda.synchronize()
+    assert c.err.item() == kb.DEV_ERR_RANGE
+
+
+@pytest.mark.parametrize("form", ["tree", "chosen pages"])
+@pytest.mark.parametrize("dtype", [kb.F16, kb.BF16])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("pages", [0, 2])
+def test_a_window_key_that_is_no_number_is_flagged(pages, value, dtype, form):
+    """One token of a short window: the largest logit of its lane is another's, or there is none."""
+    cfg = kb.Config(num_q_heads=4, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=dtype)
+    c = make(cfg, [pages], [3], 2, [2], seed=6)
+    c.d["res_k"][:, :, 1, 40] = value
+    if form == "tree":
+        call(c)
+    else:
+        sparse(c, c.q[:, 0], c.ints(np.full((1, 1, 1), 0)), c.ints([min(pages, 1)]))
+    torch.cuda.synchronize()
+    assert c.err.item() == kb.DEV_ERR_RANGE
