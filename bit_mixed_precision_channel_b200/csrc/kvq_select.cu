@@ -199,6 +199,8 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
       else
         pos += x;  // also what is no number
     }
+    // (infinite bounds of one sign are in no order, and no NaN among them shows it)
+    if (!(pos < INFINITY && neg > -INFINITY)) flag_error(p.err, KVQ_DEV_ERR_RANGE);
     const int at = key_meta_pos(tid);
     sh.wa[at] = 3.0 * pos * unbias(T());
     sh.wz[at] = (pos + neg) * unbias(T());

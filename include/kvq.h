@@ -403,8 +403,8 @@ KVQ_API kvq_status kvq_gather_tokens(const kvq_config* cfg, const void* k, const
  * int32 [batch].  A sequence with at most n_select pages keeps them all and is not scored.
  * Requires n_select >= 1, n_first + n_recent <= n_select and max_pages <= 204800
  * (KVQ_ERR_UNSUPPORTED above).  An invalid num_pages[b] sets KVQ_DEV_ERR_LENGTH and chooses
- * nothing for b; a query that is not finite sets KVQ_DEV_ERR_RANGE.  One launch, no
- * workspace; calls may overlap on the GPU if they write different sel and n_sel. */
+ * nothing for b; a query of a scored sequence that is not finite sets KVQ_DEV_ERR_RANGE.  One launch,
+ * no workspace; calls may overlap on the GPU if they write different sel and n_sel. */
 KVQ_API kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
                                     int32_t batch, const int32_t* page_table, int32_t max_pages,
                                     const int32_t* num_pages, int32_t n_first, int32_t n_recent,

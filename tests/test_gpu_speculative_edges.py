@@ -117,3 +117,26 @@ def test_a_window_key_that_is_no_number_is_flagged(pages, value, dtype, form):
         sparse(c, c.q[:, 0], c.ints(np.full((1, 1, 1), 0)), c.ints([min(pages, 1)]))
     torch.cuda.synchronize()
     assert c.err.item() == kb.DEV_ERR_RANGE
+
+
+# ---------------------------------------------------------------- choices by queries that are no finite number
+
+
+@pytest.mark.parametrize("pages", [20, 300])
+@pytest.mark.parametrize("dtype", [kb.F16, kb.BF16])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_a_choice_by_a_query_that_is_no_number_is_flagged(value, dtype, pages):
+    """Keys all above zero in the channel: every page's bound is the same infinity, not NaN."""
+    cfg = kb.Config(num_q_heads=2, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=dtype)
+    c = Cache(cfg, [pages], [0], seed=5, distinct=12)
+    for i in range(len(c.pool)):
+        K = syn.from_bits(c.tokens(32), dtype)[:, 0]
+        K[:, 7] = 1.0 + np.abs(K[:, 7])
+        c.pool[i, 0] = oracle.quantize_page(syn.to_bits(K, dtype), c.values(32)[:, 0], c.oc)
+    c.d["pool"] = torch.from_numpy(c.pool.reshape(-1)).cuda()
+    q = c.queries(1)
+    q[0, 1, 7] = bits(value, dtype)
+    sel, n_sel = run_select(c, q, 4, 0, 0)
+    torch.cuda.synchronize()
+    assert c.err.item() == kb.DEV_ERR_RANGE
+    assert n_sel.item() == 4 and (sel >= 0).all() and (sel < pages).all()
