@@ -1005,6 +1005,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                                            __vmaxu2(v[r][c].z & 0x7fff7fffu, v[r][c].w & 0x7fff7fffu)));
               const float2 m = unpack2(m2, T());
               const float top = quad_max(fmaxf(m.x, m.y));
+              // (its logits may all be minus infinity, which looks like a row that sees nothing; NaN shows in the sums)
+              if (valid[r] && !(top < INFINITY)) flag_error(p.err, KVQ_DEV_ERR_RANGE);
               // |q| < 2^e; e = 0 below 1
               const int e = min(max(int((__float_as_uint(top) >> 23) & 0xff) - 126, 0), 126);
               f[r] = p.c_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);

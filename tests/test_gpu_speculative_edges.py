@@ -140,3 +140,22 @@ def test_a_choice_by_a_query_that_is_no_number_is_flagged(value, dtype, pages):
     torch.cuda.synchronize()
     assert c.err.item() == kb.DEV_ERR_RANGE
     assert n_sel.item() == 4 and (sel >= 0).all() and (sel < pages).all()
+
+
+# ---------------------------------------------------------------- queries that are no finite number
+
+
+@pytest.mark.parametrize("T,gqa", [(2, 4), (3, 4)])
+@pytest.mark.parametrize("dtype", [kb.F16, kb.BF16])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_queries_that_are_no_number_are_flagged(value, dtype, T, gqa):
+    """Without pages, and with keys of one sign: every logit may be minus infinity, which is no number that a
+    softmax shows."""
+    cfg = kb.Config(num_q_heads=gqa, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=dtype)
+    c = make(cfg, [0], [4], T, [T], seed=4)
+    c.d["res_k"][:, :, :4, 7] = -1.0 if value > 0 else 1.0
+    c.t["k_draft"][..., 7] = -1.0 if value > 0 else 1.0
+    c.t["q"][0, 1, gqa - 1, 7] = value
+    call(c)
+    torch.cuda.synchronize()
+    assert c.err.item() == kb.DEV_ERR_RANGE
