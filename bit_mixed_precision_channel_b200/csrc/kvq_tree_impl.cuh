@@ -197,9 +197,6 @@ __device__ __forceinline__ uint32_t scaled_h2(uint32_t x, float f, __nv_bfloat16
   const float2 y = unpack2(x, __nv_bfloat16());
   return pack_h2(y.x * f, y.y * f);
 }
-__device__ __forceinline__ uint32_t half_of(uint32_t x) {  // x / 2 of an fp16 pair
-  return h2_as_u32(__hmul2(u32_as_h2(x), __float2half2_rn(0.5f)));
-}
 
 // The least integer n >= -20 with a value scale below 2^n.
 __device__ __forceinline__ float scale_log2(float s) { return float(max(-20, int((__float_as_uint(s) >> 23) & 0xff) - 126)); }
@@ -833,8 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (half == 0 && a == 0) {
           if (have && lane < 16) {  // zero points: row 128 + g of the key operand
             const uint4 z = lds128(rec + p.L.k_zero + gp * 256 + 16 * lane);
-            const uint4 o = make_uint4(half_of(meta_h2(z.x, T())), half_of(meta_h2(z.y, T())),
-                                       half_of(meta_h2(z.z, T())), half_of(meta_h2(z.w, T())));
+            const uint4 o = make_uint4(scaled_h2(z.x, 0.5f, T()), scaled_h2(z.y, 0.5f, T()),
+                                       scaled_h2(z.z, 0.5f, T()), scaled_h2(z.w, 0.5f, T()));
             *reinterpret_cast<uint4*>(smem + kKhi + tco(128 + g, lane)) = o;
             // (a scale beyond fp16 makes the sums no number; a zero point could leave a weight of
             // zero.  Looked at once, behind the loop: a flag raised here took 2% more time.)

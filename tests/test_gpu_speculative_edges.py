@@ -159,3 +159,27 @@ def test_queries_that_are_no_number_are_flagged(value, dtype, T, gqa):
     call(c)
     torch.cuda.synchronize()
     assert c.err.item() == kb.DEV_ERR_RANGE
+
+
+# ---------------------------------------------------------------- keys at the end of their range
+
+
+@pytest.mark.parametrize("lo,hi", [(-130560.0, -125000.0), (120000.0, 130560.0), (66000.0, 66000.0), (-130560.0, 300.0)])
+def test_bf16_zero_points_up_to_the_documented_range(lo, hi):
+    """Keys of a page up to 131008 in magnitude, met by a query that makes ordinary logits of them."""
+    cfg = kb.Config(num_q_heads=8, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=kb.BF16)
+    c = make(cfg, [3], [4], 4, [4], seed=21)
+    c.q[:] = 0
+    c.q[..., 7] = bits(1e-4, kb.BF16)
+    c.q[..., 8] = bits(0.5, kb.BF16)
+    c.t["q"] = to_dev(c.q, kb.BF16)
+    for s in range(3):
+        K = c.tokens(32)[:, 0]
+        K[:, 7] = syn.to_bits(c.rng.uniform(lo, hi, 32).astype(np.float32), kb.BF16)
+        K[0, 7] = bits(lo, kb.BF16)
+        c.pool[c.table[0, s], 0] = oracle.quantize_page(K, c.values(32)[:, 0], c.oc)
+    c.d["pool"] = torch.from_numpy(c.pool.reshape(-1)).cuda()
+    call(c)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    check(c)
