@@ -1177,6 +1177,12 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
       int np, rl;
       const int w = seq_weight<P>(p, b, np, rl);
       if (w < 0 && cta == 0) flag_error(p.err, KVQ_DEV_ERR_LENGTH);
+      if constexpr (SPARSE) {  // the table's length (np counts the chosen slots)
+        if (cta == 0) {
+          const int len = __ldcg(p.table_len + b);
+          if (len < 0 || len > p.table_pages) flag_error(p.err, KVQ_DEV_ERR_LENGTH);
+        }
+      }
       if (!DRAFT && w <= 0 && b % p.n_ctas == cta) {  // nothing to attend to: the output is 0
         float4* o = reinterpret_cast<float4*>(p.out + size_t(b) * p.Hq * kHeadDim);
         for (int i = 0; i < p.Hq * kHeadDim / 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);

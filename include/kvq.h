@@ -415,8 +415,8 @@ KVQ_API kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int
  * kh, attention over the pages in slots sel[b][kh][0 .. n_sel[b]) of page_table[b], followed
  * by the res_len[b] residual tokens.  sel: int32 [batch][Hkv][max_sel], as kvq_select_pages
  * writes it (or any other choice, in any order; a slot listed twice counts twice).  A slot
- * outside [0, num_pages[b]) sets KVQ_DEV_ERR_PAGE_RANGE, n_sel[b] outside [0, max_sel]
- * KVQ_DEV_ERR_LENGTH.  Everything else (q, out, workspace of
+ * outside [0, num_pages[b]) sets KVQ_DEV_ERR_PAGE_RANGE, n_sel[b] outside [0, max_sel] and
+ * num_pages[b] outside [0, max_pages] KVQ_DEV_ERR_LENGTH.  Everything else (q, out, workspace of
  * kvq_decode_workspace_bytes(cfg, batch, max_pages) bytes with its zero-counter contract,
  * precision, empty sequences, errors) as for kvq_decode_attention; the sums over the values
  * are kept near zero on the way, so they are off by less over long choices. */

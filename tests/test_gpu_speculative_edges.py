@@ -183,3 +183,21 @@ def test_bf16_zero_points_up_to_the_documented_range(lo, hi):
     torch.cuda.synchronize()
     assert c.err.item() == 0
     check(c)
+
+
+# ---------------------------------------------------------------- lengths
+
+
+def test_chosen_pages_of_a_table_of_no_valid_length_are_flagged():
+    cfg = kb.Config(num_q_heads=4, num_kv_heads=1, page_tokens=32, num_boost=16)
+    c = Cache(cfg, [9, 9], [3, 3], seed=22)
+    q = c.queries(2)
+    sel = c.ints([[[0, 4, 8]], [[1, 2, 3]]])
+    good = sparse(c, q, sel, c.ints([3, 3]))
+    assert c.err.item() == 0
+    for bad in (c.max_pages + 1, 2 ** 31 - 1, -1):
+        c.err.zero_()
+        c.d["num_pages"][1] = bad
+        out = sparse(c, q, sel, c.ints([3, 3]))
+        assert c.err.item() & kb.DEV_ERR_LENGTH
+        assert torch.equal(out[0], good[0])
