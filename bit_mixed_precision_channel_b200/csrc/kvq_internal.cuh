@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "kvq.h"
+#include "kvq_limit.cuh"
 
 namespace kvq {
 
@@ -431,15 +432,9 @@ inline cudaError_t ensure_dynamic_smem(Kernel kernel, int bytes, int (&seen)[64]
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (bytes <= __atomic_load_n(&seen[dev], __ATOMIC_ACQUIRE)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) {
-    int cur = __atomic_load_n(&seen[dev], __ATOMIC_ACQUIRE);
-    while (cur < bytes && !__atomic_compare_exchange_n(&seen[dev], &cur, bytes, false, __ATOMIC_ACQ_REL,
-                                                        __ATOMIC_ACQUIRE)) {
-    }
-  }
-  return e;
+  return cudaError_t(raise_limit(seen[dev], bytes, [kernel](int n) {
+    return int(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, n));
+  }));
 }
 size_t decode_main_bytes(int P, int GQA, uint32_t rec_bytes);
 kvq_status decode_check_args(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
