@@ -211,10 +211,10 @@ class PagedKVCache:
         the drafted tokens their mask names; see tree_attention.  The cache is not changed.  The
         first call allocates the scratch (20 MB for every tree), so it cannot be one that is captured."""
         if self.tree_workspace is None:
-            if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("verify allocates its scratch in its first call: call it once before a capture")
             need = max(kb.tree_workspace_bytes(self.cfg, self.batch, T) for T in (1, 2, 4, 8, kb.MAX_DRAFT))
             with self._on(stream):
+                if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("verify allocates its scratch in its first call: call it once before a capture")
                 self.tree_workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
         kb.tree_attention(self.cfg, self.pool, q, self.page_table, self.num_pages, self.res_k, self.res_v, self.res_len,
                           k_draft, v_draft, mask, draft_len, out, self.tree_workspace, sm_scale, self.err, stream)
