@@ -273,28 +273,29 @@ def _need(name: str, t, dtype=None, numel: int | None = None, dim: int | None = 
         raise ValueError(f"{name}: {t.numel()} elements, the call reads {numel}")
 
 
-def _need_rows(name: str, t, batch: int, row: tuple):
-    """A tensor [batch][*row] whose row length the call takes from another argument: wider rows would
-    be read with the wrong stride.  (More sequences than the batch are left alone; any other number of
-    dimensions has to hold exactly the extent.)"""
-    shape = t.shape
-    if shape == (batch, *row):
-        return
-    if len(shape) == 1 + len(row):
-        if shape[1:] != row or shape[0] < batch:
-            raise ValueError(f"{name}: shape {tuple(shape)}, the call takes {(batch, *row)}")
-    elif t.numel() != batch * math.prod(row):
-        raise ValueError(f"{name}: {t.numel()} elements, the call takes {(batch, *row)}")
+def _need_rows(name: str, t, shape: tuple):
+    """A tensor whose row length the call takes from another argument: wider rows would be read with
+    the wrong stride.  (More sequences than the batch are left alone; any other number of dimensions
+    has to hold exactly the extent.)"""
+    if t.dim() == len(shape):
+        if t.shape[1:] != shape[1:] or t.shape[0] < shape[0]:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, the call takes {shape}")
+    elif t.numel() != math.prod(shape):
+        raise ValueError(f"{name}: {t.numel()} elements, the call takes {shape}")
 
 
 def _vet(stream, *specs) -> int:
-    """_need and _cuda over (name, tensor, element type, least elements) in one pass, for the
-    calls of a decode step; returns the stream."""
+    """_need, _need_rows and _cuda over (name, tensor, element type, least elements or shape) in one
+    pass, for the calls of a decode step; returns the stream."""
     dev = cur = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
-    for name, t, dtype, numel in specs:
+    for name, t, dtype, extent in specs:
         if t is not None:
-            if t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel:
-                _need(name, t, dtype, numel)
+            if type(extent) is tuple:
+                if t.dtype is not dtype or not t.is_contiguous() or t.shape != extent:
+                    _need(name, t, dtype)
+                    _need_rows(name, t, extent)
+            elif t.dtype is not dtype or not t.is_contiguous() or t.numel() < extent:
+                _need(name, t, dtype, extent)
             if t.get_device() != cur:
                 dev = -1
     if dev < 0 or stream is not None:
@@ -575,16 +576,10 @@ def tree_attention(cfg: Config, pool, q, page_table, num_pages, res_k, res_v, re
     batch, max_pages = page_table.shape
     _need("q", q, dt, dim=4)
     T = q.shape[1]
-    rows, kv = batch * T * cfg.num_q_heads * D, batch * T * cfg.num_kv_heads * D
-    window, words = batch * cfg.num_kv_heads * cfg.page_tokens * D, (T + 31) // 32
-    q_row, kv_row = (T, cfg.num_q_heads, D), (T, cfg.num_kv_heads, D)
-    _need_rows("q", q, batch, q_row)
-    _need_rows("k_draft", k_draft, batch, kv_row)
-    _need_rows("v_draft", v_draft, batch, kv_row)
-    _need_rows("mask", mask, batch, (T, words))
-    _need_rows("out", out, batch, q_row)
+    rows, kv, words = (batch, T, cfg.num_q_heads, D), (batch, T, cfg.num_kv_heads, D), (T + 31) // 32
+    window = batch * cfg.num_kv_heads * cfg.page_tokens * D
     st = _vet(stream, ("q", q, dt, rows), ("k_draft", k_draft, dt, kv), ("v_draft", v_draft, dt, kv),
-              ("mask", mask, i32, batch * T * words), ("draft_len", draft_len, i32, batch),
+              ("mask", mask, i32, (batch, T, words)), ("draft_len", draft_len, i32, batch),
               ("out", out, torch.float32, rows), ("pool", pool, torch.uint8, 0), ("page_table", page_table, i32, 0),
               ("num_pages", num_pages, i32, batch), ("res_len", res_len, i32, batch), ("res_k", res_k, dt, window),
               ("res_v", res_v, dt, window), ("workspace", workspace, torch.uint8, 0), ("err", err, i32, 1))
@@ -605,9 +600,7 @@ def append_path(cfg: Config, k_draft, v_draft, path, n_path, taken, res_k, res_v
     i32, D = torch.int32, cfg.head_dim
     _need("path", path, i32, dim=2)
     batch, T = path.shape
-    kv, window = batch * T * cfg.num_kv_heads * D, batch * cfg.num_kv_heads * cfg.page_tokens * D
-    for name, t in (("k_draft", k_draft), ("v_draft", v_draft)):
-        _need_rows(name, t, batch, (T, cfg.num_kv_heads, D))
+    kv, window = (batch, T, cfg.num_kv_heads, D), batch * cfg.num_kv_heads * cfg.page_tokens * D
     st = _vet(stream, ("k_draft", k_draft, dt, kv), ("v_draft", v_draft, dt, kv), ("path", path, i32, 0),
               ("n_path", n_path, i32, batch), ("taken", taken, i32, batch), ("res_len", res_len, i32, batch),
               ("res_k", res_k, dt, window), ("res_v", res_v, dt, window), ("err", err, i32, 1))
