@@ -483,8 +483,8 @@ __device__ __forceinline__ void page_group(const uint8_t* rec, int grp, const La
 // One piece of n <= 16 residual tokens staged in shared memory as K rows then V rows
 // (272-byte rows; rows n..15 hold zeros).  The PV operand carries 0.5 * p so
 // that the accumulator stays in the units of the code products.  Two bf16 parts of it hold 17
-// bits; FINE adds a third (over chosen pages, where the window is a large share of the tokens) and
-// flags logits that are no finite number, one of minus infinity too.
+// bits; FINE adds a third (over chosen pages, where the window is a large share of the tokens).
+// Logits that are no finite number are flagged, one of minus infinity too.
 // DRAFT: token t of the piece is drafted token t - first when that is not negative, and seen
 // by head hd if bit t - first of mk[hd >> gqa_log2] is set.
 template <typename T, int GQA, bool DRAFT, bool FINE>
@@ -524,11 +524,11 @@ __device__ __forceinline__ void residual_piece(const uint8_t* Kr, const uint8_t*
       const float x = (acc[nt][2 * r] + acc[nt][2 * r + 1]) * c_log2;
       const int d = g + 8 * r - first;
       const bool in = (g + 8 * r) < n && (!DRAFT || d < 0 || ((see >> (d & 31)) & 1u));
-      if (FINE) bad |= in && !(fabsf(x) < INFINITY);
+      bad |= in && !(fabsf(x) < INFINITY);
       L[0][nt][r] = in ? x : -INFINITY;
     }
   }
-  if (FINE && bad) flag_error(err, KVQ_DEV_ERR_RANGE);
+  if (bad) flag_error(err, KVQ_DEV_ERR_RANGE);
   softmax_step<NT, 1>(st, L, err);
   constexpr bool kThird = std::is_same<T, __nv_bfloat16>::value;
   uint32_t pb[NT][2];
@@ -1425,7 +1425,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
           float* outu = out_base<GQA, DRAFT>(p, d.b, d.h);
           const int rows = out_rows<GQA, DRAFT>(p, d.b);
           float* part_me = p.part + (size_t(owner) + u) * GQA * kPartStride;
-          float chk = 0.0f;  // 0, or no number once a sum is none: a value that is none reaches rows that do not see it
+          float chk = 0.0f;  // 0, or no number once a sum is none
           for (int e = tid; e < GQA * kHeadDim; e += kDecodeThreads) {
             const int h = e >> 7, ch = e & 127;
             float M = -INFINITY;
@@ -1440,7 +1440,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
                 O += f * (kCodeScale * sO[(w * GQA + h) * kHeadDim + ch] + sh.zv[w][h]);
               }
             }
-            if ((DRAFT || SPARSE) && (!DRAFT || h < rows)) chk = fmaf(O, 0.0f, chk);
+            if (!DRAFT || h < rows) chk = fmaf(O, 0.0f, chk);
             if (sole) {
               if (!DRAFT || h < rows) outu[out_row<DRAFT>(p, h) + ch] = Ls > 0.0f ? O / Ls : 0.0f;
             } else {
@@ -1452,7 +1452,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (GQA <= 4 ? 4 : 2))
               }
             }
           }
-          if ((DRAFT || SPARSE) && chk != 0.0f) flag_error(p.err, KVQ_DEV_ERR_RANGE);
+          if (chk != 0.0f) flag_error(p.err, KVQ_DEV_ERR_RANGE);
           if (!sole) {
             // ---- split merge: the last of the contributors i0..i1 merges their partials.
             // The barrier orders every thread's partial writes before the counter update,
