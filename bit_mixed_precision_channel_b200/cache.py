@@ -171,9 +171,10 @@ class PagedKVCache:
         self.commit_host(flushing)
 
     # ---------------------------------------------------------------- speculative decoding
-    # A round drafts tokens with `attend_few` (or any other drafter), attends from the drafted
-    # tree to the whole cache with `verify`, and keeps what was accepted with `accept`.  The
-    # drafted tokens' keys and values stay outside the cache until then.
+    # A round attends from a drafted tree to the whole cache with `verify` and keeps what was
+    # accepted with `accept`; the drafted tokens' keys and values stay outside the cache until
+    # then.  `select` and `attend_few` are a draft step's attention over few pages and the window:
+    # they do not see tokens drafted before, which a drafter that needs them keeps itself.
 
     def select(self, q, n_select: int, n_first: int = 1, n_recent: int = 1, stream=None):
         """Chooses the n_select pages of every (sequence, KV head) whose stored key ranges
@@ -209,7 +210,8 @@ class PagedKVCache:
     def verify(self, q, k_draft, v_draft, mask, draft_len, out, sm_scale=None, stream=None):
         """Attention from the drafted tokens (q [B][T][Hq][D]) to the whole cache, the window and
         the drafted tokens their mask names; see tree_attention.  The cache is not changed.  The
-        first call allocates the scratch (20 MB for every tree), so it cannot be one that is captured."""
+        first call allocates the scratch (20 MB for every tree), so it cannot be one that is captured.
+        Layers that are not verified at once can share one: set tree_workspace to the first one's."""
         if self.tree_workspace is None:
             need = max(kb.tree_workspace_bytes(self.cfg, self.batch, T) for T in (1, 2, 4, 8, kb.MAX_DRAFT))
             with self._on(stream):
@@ -222,7 +224,8 @@ class PagedKVCache:
     def accept(self, k_draft, v_draft, path, n_path, stream=None):
         """Appends the accepted tokens path[b][:n_path[b]] (path: int32 [B][T] on the device,
         n_path: integers on the host) of k_draft, v_draft [B][T][Hkv][D] to every sequence and
-        flushes the windows they fill.  Nothing is changed if pages run out."""
+        flushes the windows they fill.  Nothing is changed if pages run out.  The lengths and the
+        pages of a flush are copied from the host, which waits for them: not for a capture."""
         P, T = self.cfg.page_tokens, path.shape[1]
         left = [int(n) for n in n_path]
         if len(left) != self.batch or any(n < 0 or n > T for n in left):

@@ -10,10 +10,9 @@
 // One cluster of up to 8 CTAs per (sequence, kv head): each CTA scores its share of the pages
 // (a warp per page, the next page's scales and zeros loading meanwhile; they, 2 KB of the
 // record's 12, are all it reads), the keys stay in shared memory, and the choice is made
-// there, so there is one launch and no workspace.  The cluster is as large as keeps all CTAs
-// resident at once: alone on the GPU 8 units finish soonest on 64 CTAs, and 512 units on
-// 1024 (fewer pages a warp would only repeat the CTAs' set-up).  Up to 256 pages, CTA 0 gathers the keys and ranks them by counting (a thread
-// per page); above, the cluster runs a radix select, 8 bits a pass, summing the CTAs'
+// there, so there is one launch and no workspace.  Few units take 8 CTAs each, many fewer (the
+// rule and its timings are at the launch).  Up to 256 pages, CTA 0 gathers the keys and ranks
+// them by counting (a thread per page); above, the cluster runs a radix select, 8 bits a pass, summing the CTAs'
 // histograms through distributed shared memory.
 //
 // The sums are carried in 64 bits: a choice is a whole-number result, and in 32 bits the
@@ -358,8 +357,11 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
 
 template <typename T, int GP, int JN>
 static cudaError_t launch_select_t(const SelectParams& p, int sms, cudaStream_t stream) {
-  // 8 CTAs an SM (512 units of 30 to 250 pages on 1, 2, 4, 8 CTAs each: 57, 51, 59, 72 us); a
-  // CTA's keys have to fit its shared memory
+  // The largest power of two up to 8 with at most 8 CTAs an SM in the grid.  At 48 to 128
+  // registers a thread 2 to 5 of them reside; the rest start as those end.  Timed on one shape,
+  // pages of 64: 512 units of 30 to 250 pages on 1, 2, 4, 8 CTAs each take 57, 51, 59, 72 us
+  // (fewer pages a warp would only repeat the CTAs' set-up), 8 units finish soonest on 64 CTAs.
+  // Long tables take more, because a CTA's keys have to fit its shared memory.
   const long long units = (long long)p.batch * p.Hkv;
   int ctas = 8;
   while (ctas > 1 && units * ctas > 8ll * sms) ctas /= 2;

@@ -327,9 +327,9 @@ KVQ_API size_t kvq_decode_workspace_bytes(const kvq_config* cfg, int32_t batch, 
  * smallest power of two above max |q| (e = 0 when |q| < 1), so a folded key operand
  * never exceeds its key scale: for fp16 caches no folded operand can overflow.  The
  * value operand p * sV is carried as p * sV * 2^-F with a per-warp exponent F that grows
- * before a value scale could overflow it.  bf16 caches: key scales and zero points enter
- * the products as fp16 — exact down to 2^-14, with an absolute error below 2^-25 under
- * it; a key scale or zero point above 65504 in magnitude (keys of magnitude above about
+ * before a value scale could overflow it.  bf16 caches: key scales, zero points and (over
+ * pages) queries enter the products as fp16 — exact down to 2^-14, with an absolute error
+ * below 2^-25 under it, so a query all of whose elements are small is met with fewer bits; a key scale or zero point above 65504 in magnitude (keys of magnitude above about
  * 10^5), or a query above 2^24, is outside the supported range and sets
  * KVQ_DEV_ERR_RANGE (the output is then undefined), as does any non-finite input. */
 KVQ_API kvq_status kvq_decode_attention(const kvq_config* cfg, const void* pool, int64_t pool_pages,
@@ -383,10 +383,12 @@ KVQ_API kvq_status kvq_gather_tokens(const kvq_config* cfg, const void* k, const
                                      int32_t* err, cudaStream_t stream);
 
 /* ---- Speculative decoding on the quantized cache ----
- * A step drafts a few tokens with attention over few pages (kvq_select_pages,
- * kvq_decode_attention_sparse), verifies the drafted tree in one pass over all of them
- * (kvq_tree_attention) and keeps the accepted path (kvq_append_path).  (The pages on the
- * method have no counterpart of these calls.) */
+ * A round takes drafted tokens, verifies their tree in one pass over the whole cache
+ * (kvq_tree_attention) and keeps the accepted path (kvq_append_path).  For the draft there is
+ * attention over few pages (kvq_select_pages, kvq_decode_attention_sparse).  It sees those
+ * pages and the window: tokens drafted so far are not in the cache, and a drafter that has
+ * to attend to them keeps them itself.  (The pages on the method have no counterpart of
+ * these calls.) */
 
 /* Choice of the pages a decode step reads.  For every sequence b and KV head h the pages
  * of page_table[b] are scored by the largest logits their stored key ranges allow, and
@@ -456,9 +458,12 @@ KVQ_API size_t kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t batch, in
  * Invalid lengths set KVQ_DEV_ERR_LENGTH, and the sequence's rows are left as they were.
  * Precision and range: up to 8 rows of a KV head (n_draft * Hq / Hkv) as for
  * kvq_decode_attention, on its kernel.  With more, half of a dequantized key (and q * 2^-e,
- * e as there) enters as fp16, the codes times their scale as a high and a low part, the
- * probabilities times their value scale as a high and a low part, sums and softmax
- * statistics in fp32; a group of keys that spans more than 130944, and a key or zero point
+ * e as there) enters as fp16, the codes times their scale as a high and a low part (so bf16
+ * zero points and window keys are exact down to 2^-13, with an absolute error below 2^-24
+ * under it); the probabilities times their value scale enter as a high and a low part, to
+ * 2^-31 of the largest probability times the largest value scale of 128 tokens; window and
+ * drafted bf16 values as fp16 relative to the token's largest, each token with its own
+ * scale; sums and softmax statistics in fp32.  A group of keys that spans more than 130944, and a key or zero point
  * above 131008 in magnitude (bf16), set KVQ_DEV_ERR_RANGE.  With any number of rows, so does
  * whatever a row sees that is not finite (the output is then undefined). */
 KVQ_API kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,

@@ -9,7 +9,7 @@ from bit_mixed_precision_channel_b200 import binding as kb
 from bit_mixed_precision_channel_b200 import synthetic as syn
 
 from _kv import to_dev
-from _spec import Cache, D
+from _spec import Cache, D, attend
 from test_gpu_select import run_select, sparse
 from test_gpu_tree import call, check, make
 
@@ -201,3 +201,50 @@ def test_chosen_pages_of_a_table_of_no_valid_length_are_flagged():
         out = sparse(c, q, sel, c.ints([3, 3]))
         assert c.err.item() & kb.DEV_ERR_LENGTH
         assert torch.equal(out[0], good[0])
+
+
+# ---------------------------------------------------------------- small queries
+
+
+@pytest.mark.parametrize("form", ["many rows", "few rows", "chosen pages"])
+def test_small_bf16_queries_on_large_keys(form):
+    """Queries of 2^-17 on keys of 4e3 (4e3 times the largest, 14, and the widest channel, 21, are inside the
+    documented range): logits from elements that fp16 holds as subnormals.
+
+    Tolerance: that of _spec.py, and an element of the query off by at most 2^-25, which moves a logit by
+    2^-25 sm_scale sum |k| and the mean by at most twice that times the distance of the values."""
+    T = dict([("many rows", 5), ("few rows", 2), ("chosen pages", 1)])[form]
+    cfg = kb.Config(num_q_heads=4, num_kv_heads=1, page_tokens=32, num_boost=16, dtype=kb.BF16)
+    c = make(cfg, [5], [7], T, [T], seed=17)
+
+    def grow(x):
+        return syn.to_bits(4e3 * syn.from_bits(x, kb.BF16).astype(np.float32), kb.BF16)
+
+    for s in range(5):
+        c.pool[c.table[0, s], 0] = oracle.quantize_page(grow(c.tokens(32))[:, 0], c.values(32)[:, 0], c.oc)
+    c.res_k[0, :, :7] = grow(c.res_k[0, :, :7])
+    c.k = grow(c.k)
+    c.q = c.queries(1, T, scale=2.0 ** -17)
+    c.d.update(pool=torch.from_numpy(c.pool.reshape(-1)).cuda(), res_k=to_dev(c.res_k, kb.BF16))
+    c.t.update(q=to_dev(c.q, kb.BF16), k_draft=to_dev(c.k, kb.BF16))
+    if form == "chosen pages":
+        out = sparse(c, c.q[:, 0], c.ints([[[0, 2, 3]]]), c.ints([3]))[:, None]
+        K, V = c.rows(0, 0, [0, 2, 3])
+    else:
+        call(c)
+        out = c.out
+        K, V = c.rows(0, 0)
+        K = np.concatenate([K, syn.from_bits(c.k[0, :, 0], kb.BF16).astype(np.float64)])
+        V = np.concatenate([V, syn.from_bits(c.v[0, :, 0], kb.BF16).astype(np.float64)])
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    out = out.cpu().numpy()
+    for i in range(T):
+        sees = np.ones(len(K), bool)
+        if form != "chosen pages":
+            sees[len(K) - T:] = c.sees[0, i]
+        for g in range(4):
+            want, tol = attend(syn.from_bits(c.q[0, i, g], kb.BF16).astype(np.float64), K, V, sees)
+            off = 2.0 ** -25 * np.abs(K).sum(1).max() / np.sqrt(D)
+            tol += 2 * off * (V.max() - V.min() + np.abs(V).max())
+            assert tol < 0.2 and np.abs(out[0, i, g] - want).max() <= tol
