@@ -329,9 +329,10 @@ KVQ_API size_t kvq_decode_workspace_bytes(const kvq_config* cfg, int32_t batch, 
  * value operand p * sV is carried as p * sV * 2^-F with a per-warp exponent F that grows
  * before a value scale could overflow it.  bf16 caches: key scales, zero points and (over
  * pages) queries enter the products as fp16 — exact down to 2^-14, with an absolute error
- * below 2^-25 under it, so a query all of whose elements are small is met with fewer bits; a key scale or zero point above 65504 in magnitude (keys of magnitude above about
- * 10^5), or a query above 2^24, is outside the supported range and sets
- * KVQ_DEV_ERR_RANGE (the output is then undefined), as does any non-finite input. */
+ * below 2^-25 under it, so a query all of whose elements are small is met with fewer bits;
+ * a key scale or zero point above 65504 in magnitude (keys of magnitude above about 10^5),
+ * or a query above 2^24, is outside the supported range and sets KVQ_DEV_ERR_RANGE (the
+ * output is then undefined), as does any non-finite input. */
 KVQ_API kvq_status kvq_decode_attention(const kvq_config* cfg, const void* pool, int64_t pool_pages,
                                 const void* q, int32_t batch,
                                 const int32_t* page_table, int32_t max_pages,
@@ -405,8 +406,9 @@ KVQ_API kvq_status kvq_gather_tokens(const kvq_config* cfg, const void* k, const
  * int32 [batch].  A sequence with at most n_select pages keeps them all and is not scored.
  * Requires n_select >= 1, n_first + n_recent <= n_select and max_pages <= 204800
  * (KVQ_ERR_UNSUPPORTED above).  An invalid num_pages[b] sets KVQ_DEV_ERR_LENGTH and chooses
- * nothing for b; a query of a scored sequence that is not finite sets KVQ_DEV_ERR_RANGE.  One launch,
- * no workspace; calls may overlap on the GPU if they write different sel and n_sel. */
+ * nothing for b; a query of a scored sequence that is not finite sets KVQ_DEV_ERR_RANGE.
+ * One launch, no workspace; calls may overlap on the GPU if they write different sel and
+ * n_sel. */
 KVQ_API kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
                                     int32_t batch, const int32_t* page_table, int32_t max_pages,
                                     const int32_t* num_pages, int32_t n_first, int32_t n_recent,
@@ -418,10 +420,10 @@ KVQ_API kvq_status kvq_select_pages(const kvq_config* cfg, const void* pool, int
  * by the res_len[b] residual tokens.  sel: int32 [batch][Hkv][max_sel], as kvq_select_pages
  * writes it (or any other choice, in any order; a slot listed twice counts twice).  A slot
  * outside [0, num_pages[b]) sets KVQ_DEV_ERR_PAGE_RANGE, n_sel[b] outside [0, max_sel] and
- * num_pages[b] outside [0, max_pages] KVQ_DEV_ERR_LENGTH.  Everything else (q, out, workspace of
- * kvq_decode_workspace_bytes(cfg, batch, max_pages) bytes with its zero-counter contract,
- * precision, empty sequences, errors) as for kvq_decode_attention; the sums over the values
- * are kept near zero on the way, so they are off by less over long choices. */
+ * num_pages[b] outside [0, max_pages] KVQ_DEV_ERR_LENGTH.  Everything else (q, out,
+ * workspace of kvq_decode_workspace_bytes(cfg, batch, max_pages) bytes with its zero-counter
+ * contract, precision, empty sequences, errors) as for kvq_decode_attention; the sums over
+ * the values are kept near zero on the way, so they are off by less over long choices. */
 KVQ_API kvq_status kvq_decode_attention_sparse(const kvq_config* cfg, const void* pool, int64_t pool_pages,
                                                const void* q, int32_t batch, const int32_t* page_table,
                                                int32_t max_pages, const int32_t* num_pages, const int32_t* sel,
@@ -463,9 +465,10 @@ KVQ_API size_t kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t batch, in
  * under it); the probabilities times their value scale enter as a high and a low part, to
  * 2^-31 of the largest probability times the largest value scale of 128 tokens; window and
  * drafted bf16 values as fp16 relative to the token's largest, each token with its own
- * scale; sums and softmax statistics in fp32.  A group of keys that spans more than 130944, and a key or zero point
- * above 131008 in magnitude (bf16), set KVQ_DEV_ERR_RANGE.  With any number of rows, so does
- * whatever a row sees that is not finite (the output is then undefined). */
+ * scale; sums and softmax statistics in fp32.  A group of keys that spans more than 130944,
+ * and a key or zero point above 131008 in magnitude (bf16), set KVQ_DEV_ERR_RANGE.  With any
+ * number of rows, so does whatever a row sees that is not finite (the output is then
+ * undefined). */
 KVQ_API kvq_status kvq_tree_attention(const kvq_config* cfg, const void* pool, int64_t pool_pages, const void* q,
                                       int32_t n_draft, int32_t batch, const int32_t* page_table,
                                       int32_t max_pages, const int32_t* num_pages, const void* res_k,

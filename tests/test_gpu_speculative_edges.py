@@ -7,6 +7,7 @@ import torch
 import oracle
 from bit_mixed_precision_channel_b200 import binding as kb
 from bit_mixed_precision_channel_b200 import synthetic as syn
+from bit_mixed_precision_channel_b200.cache import PagedKVCache
 
 from _kv import to_dev
 from _spec import Cache, D, attend
@@ -248,3 +249,28 @@ def test_small_bf16_queries_on_large_keys(form):
             off = 2.0 ** -25 * np.abs(K).sum(1).max() / np.sqrt(D)
             tol += 2 * off * (V.max() - V.min() + np.abs(V).max())
             assert tol < 0.2 and np.abs(out[0, i, g] - want).max() <= tol
+
+
+# ---------------------------------------------------------------- one scratch for two layers
+
+
+@pytest.mark.parametrize("T", [2, 30])
+def test_layers_share_the_scratch_of_the_first(T):
+    cfg = kb.Config(num_q_heads=8, num_kv_heads=2, page_tokens=32, num_boost=16)
+    layers = [PagedKVCache(cfg, 2, max_pages=16, pool_pages=32) for _ in range(2)]
+    mask = torch.full((2, T, 1), -1, dtype=torch.int32, device="cuda")
+    n = torch.full((2,), T, dtype=torch.int32, device="cuda")
+    args, want = [], []
+    for c in layers:
+        x = torch.randn(2, 9 * 32, 2, D, device="cuda").half()
+        c.prefill_batch(x, x)
+        args.append([torch.randn(2, T, h, D, device="cuda").half() for h in (8, 2, 2)])
+        want.append(torch.zeros(2, T, 8, D, device="cuda"))
+        c.verify(*args[-1], mask, n, want[-1])
+    layers[1].tree_workspace = layers[0].tree_workspace
+    for _ in range(2):
+        for c, a, w in zip(layers, args, want):
+            out = torch.zeros_like(w)
+            c.verify(*a, mask, n, out)
+            torch.cuda.synchronize()
+            assert c.check_errors() == 0 and torch.equal(out, w)
